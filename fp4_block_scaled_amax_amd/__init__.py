@@ -456,3 +456,10 @@ def update_tensor_scale(amax_running, tensor_scale, step, period=1,
                                                      int(step), int(period), float(max_safe),
                                                      _stream(stream))
     _check(st, "ue5m3fp4_update_tensor_scale")
+
+
+# The operators next to the FP4 linears (libue5m3fp4_layer.so): the 8-bit
+# block-128 linear and counter-based dropout.
+from .layer import (E4M3, E5M2, FP8_BLOCK, LAYER_LIB_PATH, Fp8Quantized, dropout,  # noqa: E402,F401
+                    dropout_backward, empty_quantized_fp8, gemm_fp8_dgrad, gemm_fp8_fprop, gemm_fp8_nt,
+                    gemm_fp8_wgrad, load_layer_library, quantize_fp8)

@@ -1,4 +1,4 @@
-"""Build libue5m3fp4.so (gfx950) in-tree with hipcc.
+"""Build libue5m3fp4.so and libue5m3fp4_layer.so (gfx950) in-tree with hipcc.
 
 Usage: python -m fp4_block_scaled_amax_amd.build   (or build() from Python)
 """
@@ -13,6 +13,9 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libue5m3fp4.so")
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemm_mx.hip"]
+# the operators next to the FP4 linears, a library of their own
+LAYER_LIB = os.path.join(PKG, "libue5m3fp4_layer.so")
+LAYER_SOURCES = ["layer/api.hip", "layer/quantize_fp8.hip", "layer/gemm_fp8.hip", "layer/dropout.hip"]
 
 HIP_FLAGS = [
     "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC",
@@ -91,7 +94,7 @@ def build(verbose=False):
     os.makedirs(objdir, exist_ok=True)
 
     def compile_one(src):
-        obj = os.path.join(objdir, src.replace(".hip", ".o"))
+        obj = os.path.join(objdir, src.replace(".hip", ".o").replace("/", "_"))
         cmd = [cc, *HIP_FLAGS, *SOURCE_FLAGS.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         out = "\n".join(l for l in (r.stdout + r.stderr).splitlines()
@@ -102,16 +105,19 @@ def build(verbose=False):
             print(out, file=sys.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(compile_one, SOURCES))
-    tmp = LIB + ".tmp"
-    r = subprocess.run([cc, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp],
-                       capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
-    os.replace(tmp, LIB)
+    sources = SOURCES + LAYER_SOURCES
+    with ThreadPoolExecutor(max_workers=len(sources)) as ex:
+        objs = dict(zip(sources, ex.map(compile_one, sources)))
+    for lib, members in ((LIB, SOURCES), (LAYER_LIB, LAYER_SOURCES)):
+        tmp = lib + ".tmp"
+        r = subprocess.run([cc, "--offload-arch=gfx950", "-shared", "-fPIC", *(objs[m] for m in members), "-o", tmp],
+                           capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
+        os.replace(tmp, lib)
     return LIB
 
 
 if __name__ == "__main__":
     print(build(verbose=True))
+    print(LAYER_LIB)

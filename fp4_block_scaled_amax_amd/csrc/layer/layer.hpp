@@ -1,0 +1,53 @@
+// Internal launch interface between the C ABI (layer/api.hip) and the
+// kernels.  Callers have validated every argument; launchers only enqueue.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ue5m3fp4 {
+
+struct QuantizeFp8Args {
+    const uint16_t* x;
+    int64_t rows, cols, ld;
+    bool e5m2, e8m0, tile;
+    uint8_t* row_codes;  // nullable pairs
+    void* row_scales;
+    uint8_t* col_codes;
+    void* col_scales;
+};
+
+void launch_quantize_fp8(const QuantizeFp8Args& a, hipStream_t stream);
+
+struct Fp8Operand {
+    const uint8_t* codes;  // [rows][K rounded up to 128]
+    const void* scales;    // [blocks][rows] or, for tiles, [blocks][ceil(rows / 128)]
+    bool e5m2, tile;
+};
+
+struct GemmFp8Args {
+    Fp8Operand a, b;
+    bool e8m0;
+    int64_t M, N, K;
+    void* c;
+    bool c_bf16;
+};
+
+void launch_gemm_fp8(const GemmFp8Args& g, hipStream_t stream);
+
+struct DropoutArgs {
+    const void* x;
+    const void* residual;  // nullable
+    void* out;
+    bool x_f32, out_f32;
+    int64_t ldx, ldr, ldo, rows, cols;
+    uint32_t threshold;  // an element is kept iff its 16 bits are >= threshold
+    float scale;
+    uint64_t seed;
+    uint32_t offset;
+    float* amax;  // nullable
+};
+
+void launch_dropout(const DropoutArgs& a, hipStream_t stream);
+
+}  // namespace ue5m3fp4

@@ -1,0 +1,119 @@
+/*
+ * libue5m3fp4_layer -- the operators next to the FP4 linears of
+ * libue5m3fp4, for AMD Instinct MI355X (gfx950):
+ *
+ *   - the 8-bit linear: quantization of bf16 tensors to E4M3 or E5M2 codes
+ *     with one scale per block of 128, and the three training GEMMs on such
+ *     operands.  The recipe of include/ue5m3fp4.h runs FP4 in the eligible
+ *     internal linears ("UE5M3 FP4 Block Scaling for Stable Language Model
+ *     Pretraining", arXiv 2609.02846, abstract); these serve the others.
+ *   - dropout from the counter-based generator of the stochastic rounding,
+ *     fused with the residual addition and the tensor amax that the periodic
+ *     tensor scale is refreshed from; the mask is never stored.
+ *
+ * Formats:
+ *   E4M3 code (byte): OCP FP8 E4M3 (bias 7, largest 448, no Inf);
+ *   E5M2 code (byte): OCP FP8 E5M2 (bias 15, largest finite 57344).
+ *   Scales: fp32 (UE5M3FP4_SCALE_F32) or one E8M0 byte, 2^(c - 127), 0xFF =
+ *   NaN (UE5M3FP4_SCALE_E8M0).
+ *   A quantized R x C operand, blocked along C:
+ *     codes  [R][Cp] bytes, Cp = C rounded up to a multiple of 128, the codes
+ *            of columns C .. Cp - 1 zero;
+ *     scales [Cp / 128][R] for 1 x 128 blocks, or [Cp / 128][ceil(R / 128)]
+ *            for 128 x 128 tiles (block index first: a GEMM step of 128 along
+ *            the contraction axis reads one contiguous run);
+ *     value(i, j) = scales[j / 128][i or i / 128] * fp8(codes[i][j]).
+ *
+ * Quantization arithmetic (fp32, round to nearest even, no fused ops): with
+ * amax the largest |x| of the block and F = 448 (E4M3) or 57344 (E5M2),
+ *   fp32 scale:  s = max(amax / F, 2^-126);
+ *   E8M0 scale:  s = the least power of two >= amax / F, at least 2^-127;
+ *   code = the nearest fp8 value (ties to even) of x * (1 / s).
+ * A block whose amax is not finite gets the scale NaN and zero codes: the
+ * GEMMs return NaN wherever it enters.
+ *
+ * Conventions: those of include/ue5m3fp4.h -- device pointers owned by the
+ * caller, every argument checked on the host before any HIP call, work
+ * enqueued on `stream` of the current device, nothing allocated, synchronized
+ * or kept; array base pointers 16-byte aligned, scalars 4-byte aligned; sizes
+ * of 0 are valid and launch nothing (except the GEMMs with K == 0, which
+ * write zeros).
+ */
+#ifndef UE5M3FP4_LAYER_H
+#define UE5M3FP4_LAYER_H
+
+#include "ue5m3fp4.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+enum ue5m3fp4_fp8_format { UE5M3FP4_E4M3 = 0, UE5M3FP4_E5M2 = 1 };
+enum ue5m3fp4_scale_type { UE5M3FP4_SCALE_F32 = 0, UE5M3FP4_SCALE_E8M0 = 1 };
+enum ue5m3fp4_data_type { UE5M3FP4_BF16 = 0, UE5M3FP4_F32 = 1 };
+
+/* Quantize a bf16 tensor x (rows x cols, row stride ld elements) to 8 bits.
+ *   format: UE5M3FP4_E4M3 or UE5M3FP4_E5M2; scale_type as above;
+ *   tile: 0 = 1 x 128 blocks along each output's own contraction axis, 1 =
+ *       one scale per aligned 128 x 128 tile of x (shared by both outputs,
+ *       whose codes are then each other's transpose);
+ *   row_codes / row_scales: x blocked along cols;
+ *   col_codes / col_scales: x^T (a cols x rows operand) blocked along rows,
+ *       from the same read of x.
+ * Each pair is both NULL or both non-NULL, at least one pair (EINVAL).  Any
+ * rows and cols below 2^31, ld >= cols (ESHAPE), rows * ld < 2^40 (ERANGE).
+ * Every byte of the outputs is written, the codes' zero padding included.
+ * x and the outputs must not overlap. */
+UE5M3FP4_API int ue5m3fp4_quantize_fp8(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, int format,
+                                       int scale_type, int tile, uint8_t* row_codes, void* row_scales,
+                                       uint8_t* col_codes, void* col_scales, void* stream);
+
+/* C[i][j] = sum_k A(i, k) B(j, k) of two 8-bit operands blocked along K, fp32
+ * accumulation: A is M x K, B is N x K.
+ *   a_format, b_format: the operands' formats, in any combination;
+ *   a_tile, b_tile: 1 x 128 blocks (0) or 128 x 128 tiles (1) of each;
+ *   scale_type: common to both operands;
+ *   c: [M][N] (row stride N) fp32 (UE5M3FP4_F32) or bf16 (UE5M3FP4_BF16,
+ *       rounded once to nearest even).
+ * Any M, N, K below 2^31 with M*N, M*K, N*K < 2^40 (ERANGE).  The product of
+ * the two scales of a block pair has to be finite in fp32. */
+UE5M3FP4_API int ue5m3fp4_gemm_fp8_nt(const uint8_t* a_codes, const void* a_scales, int a_format, int a_tile,
+                                      const uint8_t* b_codes, const void* b_scales, int b_format, int b_tile,
+                                      int scale_type, int64_t M, int64_t N, int64_t K, void* c, int c_type,
+                                      void* stream);
+
+/* out = residual + dropout(x): element (i, j) of a rows x cols tensor has
+ * e = i * cols + j; call n = e >> 3 of Philox4x32-10 (Salmon et al., SC'11)
+ * with counter (n lo, n hi, offset, 2) and key (seed lo, seed hi) gives it
+ * the low (e even) or high (e odd) 16 bits u of word (e & 7) >> 1 (the layout
+ * of the stochastic rounding, whose streams have third counter words 0 and
+ * 1).  With t = p * 65536 rounded to the nearest integer, ties to even, the
+ * element is kept iff u >= t:
+ *   y = kept ? x * fp32(65536 / (65536 - t)) : 0;  out = residual + y,
+ * each an fp32 operation, rounded once to out's type.  A dropped element
+ * contributes 0 whatever x holds, NaN and Inf included; t = 65536 drops all.
+ *   x, out: bf16 or fp32 (x_type, out_type); residual: nullable, of out's
+ *       type; row strides ldx, ldr, ldo in elements (each >= cols; ldr is
+ *       not read without a residual).
+ *   p in [0, 1] (EINVAL otherwise);
+ *   amax_inout: nullable device fp32; receives max(*amax_inout, max|out|) over
+ *       the stored values (a NaN propagates).
+ * out may be x or residual itself where the types and strides agree; other
+ * overlaps are not allowed.  rows, cols < 2^31, rows * ld < 2^40 (ERANGE). */
+UE5M3FP4_API int ue5m3fp4_dropout(const void* x, int x_type, int64_t ldx, const void* residual, int64_t ldr,
+                                  void* out, int out_type, int64_t ldo, int64_t rows, int64_t cols, double p,
+                                  uint64_t seed, uint32_t offset, float* amax_inout, void* stream);
+
+/* The gradient of ue5m3fp4_dropout with respect to x: the mask of the same
+ * (p, seed, offset) and shape is generated again, dx = kept ? dy * fp32(65536
+ * / (65536 - t)) : 0.  (The gradient with respect to the residual is dy.)
+ * Arguments as there. */
+UE5M3FP4_API int ue5m3fp4_dropout_backward(const void* dy, int dy_type, int64_t lddy, void* dx, int dx_type,
+                                           int64_t lddx, int64_t rows, int64_t cols, double p, uint64_t seed,
+                                           uint32_t offset, float* amax_inout, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* UE5M3FP4_LAYER_H */
