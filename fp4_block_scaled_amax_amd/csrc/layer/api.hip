@@ -12,6 +12,7 @@ using namespace ue5m3fp4;
 
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
+constexpr int64_t kMaxFp8K = (int64_t)1 << 24;  // a GEMM tile's code offsets fit 32 bits
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
@@ -81,7 +82,7 @@ int ue5m3fp4_gemm_fp8_nt(const uint8_t* a_codes, const void* a_scales, int a_for
     if (M < 0 || N < 0 || K < 0 || !is01(a_format) || !is01(b_format) || !is01(a_tile) || !is01(b_tile) ||
         !is01(scale_type) || !is01(c_type))
         return UE5M3FP4_EINVAL;
-    if (M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return UE5M3FP4_ERANGE;
+    if (M >= kMaxDim || N >= kMaxDim || K >= kMaxFp8K) return UE5M3FP4_ERANGE;
     const int64_t Kp = (K + 127) / 128 * 128;
     if (M * N >= kMaxElems || M * Kp >= kMaxElems || N * Kp >= kMaxElems) return UE5M3FP4_ERANGE;
     if (M == 0 || N == 0) return UE5M3FP4_OK;  // nothing is read or written

@@ -17,11 +17,12 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 512;
 constexpr int kGroupM = 4;
+constexpr int kSchedMfma = 0x008, kSchedValu = 0x002, kSchedDs = 0x100;
 
 // How a block's scales reach the accumulators.
 enum ScaleMode {
-    kTileB,    // fp32 (or decoded) scales, one per wave for B: a factor per lane
-    kVectorB,  // fp32 (or decoded) scales, one per row of B: a factor per element
+    kTileB,    // one scale per wave for B: a factor per lane
+    kVectorB,  // one scale per row of B: a factor per element
     kHardware  // E8M0 scales as operands of the matrix instruction
 };
 
@@ -41,9 +42,23 @@ __device__ __forceinline__ float e8m0_value(uint32_t c) {
     return c == 0xFFu ? __uint_as_float(0x7FC00000u) : c == 0u ? 0x1p-127f : __uint_as_float(c << 23);
 }
 
-__device__ __forceinline__ void load_lds16(const uint8_t* src, uint8_t* dst) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                     (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+// The same address in every lane, as scalar registers.
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+    const uint64_t v = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+    return (const uint8_t*)(((uint64_t)hi << 32) | lo);
+}
+
+// 16 bytes per lane from base + off straight to LDS: lane l's at lds + 16 l.
+// In assembly because the compiler, which cannot tell the two halves of the
+// double buffer apart, would wait for the load at the next LDS read; it has no
+// register output, and wait_staged() below waits for it.
+__device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void wait_staged() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 
 // 8 codes as fp16 (exact).
@@ -84,12 +99,27 @@ struct Frag<true, E5M2> {
     }
 };
 
-template <bool EXACT, bool AE5, bool BE5, int SC, int MI, int NI>
+// The scaled instruction; its byte selectors are immediates.
+template <bool BE5, bool AE5>
+__device__ __forceinline__ f32x4 mfma_scaled(int jb, int ib, i32x8 b, i32x8 a, f32x4 acc, uint32_t xb, uint32_t xa) {
+#define UE5M3FP4_CASE(J, I)         \
+    if (jb == J && ib == I)         \
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, acc, BE5, AE5, J, (int)xb, I, (int)xa);
+#define UE5M3FP4_CASES(J) UE5M3FP4_CASE(J, 0) UE5M3FP4_CASE(J, 1) UE5M3FP4_CASE(J, 2) UE5M3FP4_CASE(J, 3)
+    UE5M3FP4_CASES(0) UE5M3FP4_CASES(1) UE5M3FP4_CASES(2) UE5M3FP4_CASES(3)
+#undef UE5M3FP4_CASES
+#undef UE5M3FP4_CASE
+    return acc;
+}
+
+template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MI, int NI>
 __global__ __launch_bounds__(kThreads, 1) void gemm_fp8_kernel(GemmFp8Args g) {
+    static_assert(SC != kHardware || (E8M0 && !EXACT), "hardware scales are E8M0 bytes of the 8-bit instruction");
     constexpr int BM = 64 * MI, BN = 32 * NI, WM = 16 * MI, WN = 16 * NI;
     constexpr int kStage = (BM + BN) * 128;
+    typedef float scales_a __attribute__((ext_vector_type(MI)));
     __shared__ __align__(1024) uint8_t smem[2 * kStage];
-    __shared__ __align__(16) float sb_lds[SC == kVectorB ? 2 * BN : 4];
+    __shared__ __align__(16) float scales[2 * (BM + BN)];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -104,72 +134,65 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_fp8_kernel(GemmFp8Args g) {
 
     // ---- staging: one 1 KB load to LDS covers 8 rows x 128 codes; lane (r, p)
     // = (lane / 8, lane % 8) brings 16-byte unit p ^ (row / 2 % 8) of its row,
-    // so that 16 rows' reads of one unit touch every bank once.
+    // so that 16 rows' reads of one unit touch every bank once.  Offsets from
+    // the tile's first code fit 32 bits (K < 2^24).
     constexpr int LA = BM / 64, LB = BN / 64;
-    const uint8_t* pa[LA];
-    const uint8_t* pb[LB];
+    uint32_t oa[LA], ob[LB];
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
         const int row = (wave * LA + i) * 8 + (lane >> 3);
-        pa[i] = g.a.codes + min(m0 + row, g.M - 1) * Kp + 16 * ((lane & 7) ^ ((row >> 1) & 7));
+        oa[i] = (uint32_t)min((int64_t)row, g.M - 1 - m0) * (uint32_t)Kp + 16 * ((lane & 7) ^ ((row >> 1) & 7));
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
         const int row = (wave * LB + i) * 8 + (lane >> 3);
-        pb[i] = g.b.codes + min(n0 + row, g.N - 1) * Kp + 16 * ((lane & 7) ^ ((row >> 1) & 7));
+        ob[i] = (uint32_t)min((int64_t)row, g.N - 1 - n0) * (uint32_t)Kp + 16 * ((lane & 7) ^ ((row >> 1) & 7));
     }
-    auto stage = [&](int buf) __attribute__((always_inline)) {
-        uint8_t* base = smem + buf * kStage;
+    const uint8_t* ta = g.a.codes + m0 * Kp;
+    const uint8_t* tb = g.b.codes + n0 * Kp;
+    auto stage = [&](int k) __attribute__((always_inline)) {
+        const uint32_t base = lds_address(smem) + (k & 1) * kStage;
+        const uint8_t* ka = uniform(ta + (int64_t)k * 128);
+        const uint8_t* kb = uniform(tb + (int64_t)k * 128);
 #pragma unroll
-        for (int i = 0; i < LA; ++i) {
-            load_lds16(pa[i], base + (wave * LA + i) * 1024);
-            pa[i] += 128;
-        }
+        for (int i = 0; i < LA; ++i) load_lds16(ka, oa[i], base + (wave * LA + i) * 1024);
 #pragma unroll
-        for (int i = 0; i < LB; ++i) {
-            load_lds16(pb[i], base + BM * 128 + (wave * LB + i) * 1024);
-            pb[i] += 128;
-        }
+        for (int i = 0; i < LB; ++i) load_lds16(kb, ob[i], base + BM * 128 + (wave * LB + i) * 1024);
     };
 
-    // ---- scales.  A: one per lane and 16-row tile (row c).  B: one per wave
-    // (kTileB), or a row of BN in LDS (kVectorB), or one per lane and tile
-    // (kHardware).
-    const int64_t as_step = g.a.tile ? (g.M + 127) / 128 : g.M, bs_step = g.b.tile ? (g.N + 127) / 128 : g.N;
-    int64_t as_at[MI], bs_at[SC == kHardware ? NI : 1];
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        const int64_t m = min(m0 + wm * WM + 16 * i + c, g.M - 1);
-        as_at[i] = g.a.tile ? m >> 7 : m;
+    // ---- scales: thread t < BM + BN brings the scale of row t of A, then B,
+    // a block ahead, and leaves it in LDS where the lanes read theirs at once:
+    // A's as [16-row column c][tile i] of each wave row, B's by row (fp32) or
+    // like A's (hardware).
+    constexpr int kScaleBytes = E8M0 ? 1 : 4;
+    const uint8_t* sp = nullptr;
+    int64_t sstep = 0;
+    int sput = 0;
+    if (tid < BM) {
+        const int64_t m = min(m0 + tid, g.M - 1);
+        sstep = (g.a.tile ? (g.M + 127) / 128 : g.M) * kScaleBytes;
+        sp = (const uint8_t*)g.a.scales + (g.a.tile ? m >> 7 : m) * kScaleBytes;
+        sput = (tid / WM) * WM + (tid & 15) * MI + (tid % WM) / 16;
+    } else if (tid < BM + BN) {
+        const int r = tid - BM;
+        const int64_t n = min(n0 + r, g.N - 1);
+        sstep = (g.b.tile ? (g.N + 127) / 128 : g.N) * kScaleBytes;
+        sp = (const uint8_t*)g.b.scales + (g.b.tile ? n >> 7 : n) * kScaleBytes;
+        sput = SC == kHardware ? (r / WN) * WN + (r & 15) * NI + (r % WN) / 16 : r;
+        sput += BM;
     }
-    if constexpr (SC == kHardware) {
-#pragma unroll
-        for (int j = 0; j < NI; ++j) {
-            const int64_t n = min(n0 + wn * WN + 16 * j + c, g.N - 1);
-            bs_at[j] = g.b.tile ? n >> 7 : n;
+    uint32_t sreg = 0u;
+    auto load_scale = [&]() __attribute__((always_inline)) {
+        if (BM + BN >= kThreads || tid < BM + BN) {
+            if constexpr (E8M0) sreg = *sp;
+            else sreg = *(const uint32_t*)sp;
+            sp += sstep;
         }
-    } else if constexpr (SC == kTileB) {
-        bs_at[0] = min(n0 + wn * WN, g.N - 1) >> 7;
-    } else {
-        const int64_t n = min(n0 + min(tid, BN - 1), g.N - 1);
-        bs_at[0] = g.b.tile ? n >> 7 : n;
-    }
-    auto scale_f32 = [&](const void* base, int64_t at) __attribute__((always_inline)) {
-        return g.e8m0 ? e8m0_value(((const uint8_t*)base)[at]) : ((const float*)base)[at];
     };
-    float sa[MI], sb = 0.0f;
-    int ha[MI], hb[SC == kHardware ? NI : 1];
-    auto load_scales = [&](int kb) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            if constexpr (SC == kHardware) ha[i] = ((const uint8_t*)g.a.scales)[kb * as_step + as_at[i]];
-            else sa[i] = scale_f32(g.a.scales, kb * as_step + as_at[i]);
-        }
-        if constexpr (SC == kHardware) {
-#pragma unroll
-            for (int j = 0; j < NI; ++j) hb[j] = ((const uint8_t*)g.b.scales)[kb * bs_step + bs_at[j]];
-        } else {
-            sb = scale_f32(g.b.scales, kb * bs_step + bs_at[0]);
+    auto put_scale = [&](int k) __attribute__((always_inline)) {
+        if (BM + BN >= kThreads || tid < BM + BN) {
+            if constexpr (SC == kHardware) ((uint8_t*)scales)[(k & 1) * (BM + BN) + sput] = (uint8_t)sreg;
+            else scales[(k & 1) * (BM + BN) + sput] = E8M0 ? e8m0_value(sreg) : __uint_as_float(sreg);
         }
     };
 
@@ -185,63 +208,105 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_fp8_kernel(GemmFp8Args g) {
 
     if (nchunks > 0) {
         stage(0);
-        load_scales(0);
+        load_scale();
     }
     for (int k = 0; k < nchunks; ++k) {
-        if constexpr (SC == kVectorB) {
-            if (tid < BN) sb_lds[(k & 1) * BN + tid] = sb;
-        }
-        __builtin_amdgcn_s_waitcnt(0);  // this wave's share of chunk k (and its scales) is in LDS
+        put_scale(k);
+        wait_staged();  // this wave's share of chunk k is in LDS
         __syncthreads();
-        float fa[MI];
-        int xa[MI], xb[SC == kHardware ? NI : 1];
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            if constexpr (SC == kHardware) xa[i] = ha[i];
-            else fa[i] = SC == kTileB ? sa[i] * sb : sa[i];
-        }
-        if constexpr (SC == kHardware) {
-#pragma unroll
-            for (int j = 0; j < NI; ++j) xb[j] = hb[j];
-        }
         if (k + 1 < nchunks) {
-            stage((k + 1) & 1);
-            load_scales(k + 1);
+            stage(k + 1);
+            load_scale();
         }
         const uint8_t* base = smem + (k & 1) * kStage;
-        const float* sbv = sb_lds + (SC == kVectorB ? (k & 1) * BN + wn * WN + 4 * q : 0);
+        const float* sc = scales + (k & 1) * (BM + BN);
+
         Frag<EXACT, AE5> a[MI];
+        Frag<EXACT, BE5> b[2];
+        f32x4 part[2][MI], sv[2];
+        scales_a fa;
+        uint32_t xa = 0u;
+        u32x2 xb = {0u, 0u};
+        if constexpr (SC == kHardware) {
+            const uint8_t* bytes = (const uint8_t*)scales + (k & 1) * (BM + BN);
+            if constexpr (MI == 4) xa = *reinterpret_cast<const uint32_t*>(bytes + wm * WM + c * MI);
+            else xa = *reinterpret_cast<const uint16_t*>(bytes + wm * WM + c * MI);
+            if constexpr (NI == 8) xb = *reinterpret_cast<const u32x2*>(bytes + BM + wn * WN + c * NI);
+            else xb.x = *reinterpret_cast<const uint32_t*>(bytes + BM + wn * WN + c * NI);
+        } else {
+            fa = *reinterpret_cast<const scales_a*>(sc + wm * WM + c * MI);
+            if constexpr (SC == kTileB) fa *= sc[BM + wn * WN];
+        }
+        auto raw_b = [&](int j, i32x4& x, i32x4& y) __attribute__((always_inline)) {
+            x = *reinterpret_cast<const i32x4*>(base + b_base + j * 2048 + o0);
+            y = *reinterpret_cast<const i32x4*>(base + b_base + j * 2048 + o1);
+        };
+        auto read_sv = [&](int j) __attribute__((always_inline)) {
+            if constexpr (SC == kVectorB) sv[j & 1] = *reinterpret_cast<const f32x4*>(sc + BM + wn * WN + 4 * q + 16 * j);
+        };
+        auto add_part = [&](int j, int i, const f32x4& p) __attribute__((always_inline)) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[j][i][e] = __builtin_fmaf(p[e], SC == kVectorB ? sv[j & 1][e] * fa[i] : fa[i], acc[j][i][e]);
+        };
+        i32x4 x, y;
+        raw_b(0, x, y);
+        b[0].set(x, y);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
             a[i].set(*reinterpret_cast<const i32x4*>(base + a_base + i * 2048 + o0),
                      *reinterpret_cast<const i32x4*>(base + a_base + i * 2048 + o1));
+        if constexpr (EXACT) {
+            // widened fragments leave room for one of B and two partial sums
+            f32x4 p[2];
 #pragma unroll
-        for (int j = 0; j < NI; ++j) {
-            Frag<EXACT, BE5> b;
-            b.set(*reinterpret_cast<const i32x4*>(base + b_base + j * 2048 + o0),
-                  *reinterpret_cast<const i32x4*>(base + b_base + j * 2048 + o1));
-            f32x4 sv;
-            if constexpr (SC == kVectorB) sv = *reinterpret_cast<const f32x4*>(sbv + 16 * j);
+            for (int j = 0; j < NI; ++j) {
+                if (j + 1 < NI) raw_b(j + 1, x, y);
+                read_sv(j);
 #pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                if constexpr (EXACT) {
-                    f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int i = 0; i < MI; ++i) {
+                    f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.v[s], a[i].v[s], part, 0, 0, 0);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[j][i][e] = __builtin_fmaf(part[e], SC == kVectorB ? sv[e] * fa[i] : fa[i], acc[j][i][e]);
-                } else if constexpr (SC == kHardware) {
-                    acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a[i].v, acc[j][i], BE5, AE5, 0, xb[j],
-                                                                                 0, xa[i]);
-                } else {
-                    f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
-                    part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a[i].v, part, BE5, AE5, 0, 0, 0, 0);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[j][i][e] = __builtin_fmaf(part[e], SC == kVectorB ? sv[e] * fa[i] : fa[i], acc[j][i][e]);
+                    for (int s = 0; s < 4; ++s) z = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[0].v[s], a[i].v[s], z, 0, 0, 0);
+                    p[i & 1] = z;
+                    if (i > 0) add_part(j, i - 1, p[(i - 1) & 1]);
+                    else if (j > 0) add_part(j - 1, MI - 1, p[1]);
                 }
+                if (j + 1 < NI) b[0].set(x, y);
+            }
+            add_part(NI - 1, MI - 1, p[1]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+                if (j + 1 < NI) {
+                    raw_b(j + 1, x, y);
+                    b[(j + 1) & 1].set(x, y);
+                }
+                read_sv(j);
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    if constexpr (SC == kHardware) {
+                        // byte i of xa, byte j of xb
+                        acc[j][i] = mfma_scaled<BE5, AE5>(j & 3, i, b[j & 1].v, a[i].v, acc[j][i], j < 4 ? xb.x : xb.y, xa);
+                    } else {
+                        f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+                        part[j & 1][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j & 1].v, a[i].v, z, BE5, AE5, 0, 0, 0, 0);
+                        if (j > 0) add_part(j - 1, i, part[(j - 1) & 1][i]);
+                    }
+                }
+            }
+            if constexpr (SC != kHardware) {
+#pragma unroll
+                for (int i = 0; i < MI; ++i) add_part(NI - 1, i, part[(NI - 1) & 1][i]);
+            }
+        }
+        if constexpr (SC != kHardware && !EXACT) {
+            __builtin_amdgcn_sched_group_barrier(kSchedDs, 3 + 2 * MI + (SC == kVectorB), 0);
+#pragma unroll
+            for (int t = 0; t < NI * MI; ++t) {
+                __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+                if (t % MI == 0) __builtin_amdgcn_sched_group_barrier(kSchedDs, 2 + (SC == kVectorB), 0);
+                __builtin_amdgcn_sched_group_barrier(kSchedValu, SC == kVectorB ? 8 : 4, 0);
             }
         }
     }
@@ -274,22 +339,28 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_fp8_kernel(GemmFp8Args g) {
     }
 }
 
-template <bool EXACT, bool AE5, bool BE5, int SC>
+template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0>
 void launch_size(const GemmFp8Args& g, hipStream_t stream) {
     const int64_t large = ((g.M + 255) / 256) * ((g.N + 255) / 256);
     if (large >= 192) {
-        hipLaunchKernelGGL((gemm_fp8_kernel<EXACT, AE5, BE5, SC, 4, 8>), dim3((unsigned)large), dim3(kThreads), 0, stream, g);
+        hipLaunchKernelGGL((gemm_fp8_kernel<EXACT, AE5, BE5, SC, E8M0, 4, 8>), dim3((unsigned)large), dim3(kThreads), 0, stream, g);
     } else {
         const int64_t tiles = ((g.M + 127) / 128) * ((g.N + 127) / 128);
-        hipLaunchKernelGGL((gemm_fp8_kernel<EXACT, AE5, BE5, SC, 2, 4>), dim3((unsigned)tiles), dim3(kThreads), 0, stream, g);
+        hipLaunchKernelGGL((gemm_fp8_kernel<EXACT, AE5, BE5, SC, E8M0, 2, 4>), dim3((unsigned)tiles), dim3(kThreads), 0, stream, g);
     }
+}
+
+template <bool EXACT, bool AE5, bool BE5, bool E8M0>
+void launch_scales(const GemmFp8Args& g, hipStream_t stream) {
+    if constexpr (E8M0 && !EXACT) launch_size<false, AE5, BE5, kHardware, true>(g, stream);
+    else if (g.b.tile) launch_size<EXACT, AE5, BE5, kTileB, E8M0>(g, stream);
+    else launch_size<EXACT, AE5, BE5, kVectorB, E8M0>(g, stream);
 }
 
 template <bool AE5, bool BE5>
 void launch_formats(const GemmFp8Args& g, hipStream_t stream) {
-    if (!g.c_bf16) g.b.tile ? launch_size<true, AE5, BE5, kTileB>(g, stream) : launch_size<true, AE5, BE5, kVectorB>(g, stream);
-    else if (g.e8m0) launch_size<false, AE5, BE5, kHardware>(g, stream);
-    else g.b.tile ? launch_size<false, AE5, BE5, kTileB>(g, stream) : launch_size<false, AE5, BE5, kVectorB>(g, stream);
+    if (g.c_bf16) g.e8m0 ? launch_scales<false, AE5, BE5, true>(g, stream) : launch_scales<false, AE5, BE5, false>(g, stream);
+    else g.e8m0 ? launch_scales<true, AE5, BE5, true>(g, stream) : launch_scales<true, AE5, BE5, false>(g, stream);
 }
 
 }  // namespace

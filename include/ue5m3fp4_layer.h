@@ -75,8 +75,8 @@ UE5M3FP4_API int ue5m3fp4_quantize_fp8(const uint16_t* x, int64_t rows, int64_t 
  *   scale_type: common to both operands;
  *   c: [M][N] (row stride N) fp32 (UE5M3FP4_F32) or bf16 (UE5M3FP4_BF16,
  *       rounded once to nearest even).
- * Any M, N, K below 2^31 with M*N, M*K, N*K < 2^40 (ERANGE).  The product of
- * the two scales of a block pair has to be finite in fp32. */
+ * Any M, N below 2^31 and K below 2^24 with M*N, M*K, N*K < 2^40 (ERANGE).
+ * The product of the two scales of a block pair has to be finite in fp32. */
 UE5M3FP4_API int ue5m3fp4_gemm_fp8_nt(const uint8_t* a_codes, const void* a_scales, int a_format, int a_tile,
                                       const uint8_t* b_codes, const void* b_scales, int b_format, int b_tile,
                                       int scale_type, int64_t M, int64_t N, int64_t K, void* c, int c_type,

@@ -66,6 +66,7 @@ def test_gemm_argument_checks(L):
     for k in ("ac", "as_", "bc", "bs", "c"):
         assert gm(L, **{k: None}) == EINVAL
         assert gm(L, **{k: P + 8}) == EALIGN
+    assert gm(L, K=1 << 24) == ERANGE
     assert gm(L, M=1 << 31) == ERANGE and gm(L, M=1 << 20, N=1 << 20) == ERANGE
     assert gm(L, M=(1 << 31) - 1, N=1, K=1 << 10) == ERANGE
     assert gm(L, M=0, c=None) == OK and gm(L, N=0, c=None) == OK
