@@ -15,7 +15,6 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 512;
 constexpr int kGroupM = 4;
 constexpr int kSchedMfma = 0x008, kSchedValu = 0x002, kSchedDs = 0x100;
 
@@ -112,10 +111,10 @@ __device__ __forceinline__ f32x4 mfma_scaled(int jb, int ib, i32x8 b, i32x8 a, f
     return acc;
 }
 
-template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MI, int NI>
-__global__ __launch_bounds__(kThreads, 1) void gemm_fp8_kernel(GemmFp8Args g) {
+template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MW, int MI, int NI>
+__global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
     static_assert(SC != kHardware || (E8M0 && !EXACT), "hardware scales are E8M0 bytes of the 8-bit instruction");
-    constexpr int BM = 64 * MI, BN = 32 * NI, WM = 16 * MI, WN = 16 * NI;
+    constexpr int kThreads = MW * 128, WM = 16 * MI, WN = 16 * NI, BM = MW * WM, BN = 2 * WN;
     constexpr int kStage = (BM + BN) * 128;
     typedef float scales_a __attribute__((ext_vector_type(MI)));
     __shared__ __align__(1024) uint8_t smem[2 * kStage];
@@ -136,7 +135,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_fp8_kernel(GemmFp8Args g) {
     // = (lane / 8, lane % 8) brings 16-byte unit p ^ (row / 2 % 8) of its row,
     // so that 16 rows' reads of one unit touch every bank once.  Offsets from
     // the tile's first code fit 32 bits (K < 2^24).
-    constexpr int LA = BM / 64, LB = BN / 64;
+    constexpr int LA = BM / (16 * MW), LB = BN / (16 * MW);
     uint32_t oa[LA], ob[LB];
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
@@ -339,15 +338,19 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_fp8_kernel(GemmFp8Args g) {
     }
 }
 
+template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MW, int MI, int NI>
+void launch_tiled(const GemmFp8Args& g, hipStream_t stream) {
+    constexpr int BM = MW * 16 * MI, BN = 32 * NI;
+    const int64_t tiles = ((g.M + BM - 1) / BM) * ((g.N + BN - 1) / BN);
+    hipLaunchKernelGGL((gemm_fp8_kernel<EXACT, AE5, BE5, SC, E8M0, MW, MI, NI>), dim3((unsigned)tiles), dim3(MW * 128), 0,
+                       stream, g);
+}
+
 template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0>
 void launch_size(const GemmFp8Args& g, hipStream_t stream) {
     const int64_t large = ((g.M + 255) / 256) * ((g.N + 255) / 256);
-    if (large >= 192) {
-        hipLaunchKernelGGL((gemm_fp8_kernel<EXACT, AE5, BE5, SC, E8M0, 4, 8>), dim3((unsigned)large), dim3(kThreads), 0, stream, g);
-    } else {
-        const int64_t tiles = ((g.M + 127) / 128) * ((g.N + 127) / 128);
-        hipLaunchKernelGGL((gemm_fp8_kernel<EXACT, AE5, BE5, SC, E8M0, 2, 4>), dim3((unsigned)tiles), dim3(kThreads), 0, stream, g);
-    }
+    if (large >= 192 && !EXACT) launch_tiled<EXACT, AE5, BE5, SC, E8M0, 4, 4, 8>(g, stream);
+    else launch_tiled<EXACT, AE5, BE5, SC, E8M0, 2, 4, 4>(g, stream);
 }
 
 template <bool EXACT, bool AE5, bool BE5, bool E8M0>
