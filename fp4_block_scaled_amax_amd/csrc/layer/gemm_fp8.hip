@@ -10,7 +10,7 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -55,7 +55,19 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
 __device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
 }
-__device__ __forceinline__ void wait_staged() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// The same for one dword (or, zero-extended, one byte): lane l's at lds + 4 l.
+template <bool BYTE>
+__device__ __forceinline__ void load_lds_scale(const uint8_t* base, uint32_t off, uint32_t lds) {
+    if constexpr (BYTE)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+// Waits until at most N of this wave's loads are in flight.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
@@ -98,27 +110,30 @@ struct Frag<true, E5M2> {
     }
 };
 
-// The scaled instruction; its byte selectors are immediates.
-template <bool BE5, bool AE5>
-__device__ __forceinline__ f32x4 mfma_scaled(int jb, int ib, i32x8 b, i32x8 a, f32x4 acc, uint32_t xb, uint32_t xa) {
-#define UE5M3FP4_CASE(J, I)         \
-    if (jb == J && ib == I)         \
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, acc, BE5, AE5, J, (int)xb, I, (int)xa);
-#define UE5M3FP4_CASES(J) UE5M3FP4_CASE(J, 0) UE5M3FP4_CASE(J, 1) UE5M3FP4_CASE(J, 2) UE5M3FP4_CASE(J, 3)
-    UE5M3FP4_CASES(0) UE5M3FP4_CASES(1) UE5M3FP4_CASES(2) UE5M3FP4_CASES(3)
-#undef UE5M3FP4_CASES
-#undef UE5M3FP4_CASE
-    return acc;
+// Columns n .. n + 3 of row m of C, those that exist.
+__device__ __forceinline__ void store4(const GemmFp8Args& g, int64_t m, int64_t n, f32x4 v) {
+    if (g.N % 4 == 0) {
+        if (n >= g.N) return;
+        if (g.c_bf16)
+            *reinterpret_cast<bf16x4*>((__bf16*)g.c + m * g.N + n) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+        else
+            *reinterpret_cast<f32x4*>((float*)g.c + m * g.N + n) = v;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (n + e >= g.N) continue;
+        if (g.c_bf16) ((__bf16*)g.c)[m * g.N + n + e] = (__bf16)v[e];
+        else ((float*)g.c)[m * g.N + n + e] = v[e];
+    }
 }
 
-template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MW, int MI, int NI>
+template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MW, int MI, int NI, int STAGES>
 __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
     static_assert(SC != kHardware || (E8M0 && !EXACT), "hardware scales are E8M0 bytes of the 8-bit instruction");
-    constexpr int kThreads = MW * 128, WM = 16 * MI, WN = 16 * NI, BM = MW * WM, BN = 2 * WN;
-    constexpr int kStage = (BM + BN) * 128;
-    typedef float scales_a __attribute__((ext_vector_type(MI)));
-    __shared__ __align__(1024) uint8_t smem[2 * kStage];
-    __shared__ __align__(16) float scales[2 * (BM + BN)];
+    constexpr int WM = 16 * MI, WN = 16 * NI, BM = MW * WM, BN = 2 * WN;
+    constexpr int kCodes = (BM + BN) * 128, kStage = kCodes + (BM + BN) * 4;
+    __shared__ __align__(1024) uint8_t smem[STAGES * kStage];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -135,7 +150,7 @@ __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
     // = (lane / 8, lane % 8) brings 16-byte unit p ^ (row / 2 % 8) of its row,
     // so that 16 rows' reads of one unit touch every bank once.  Offsets from
     // the tile's first code fit 32 bits (K < 2^24).
-    constexpr int LA = BM / (16 * MW), LB = BN / (16 * MW);
+    constexpr int LA = BM / (16 * MW), LB = BN / (16 * MW), kLoads = LA + LB + 1;
     uint32_t oa[LA], ob[LB];
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
@@ -149,50 +164,26 @@ __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
     }
     const uint8_t* ta = g.a.codes + m0 * Kp;
     const uint8_t* tb = g.b.codes + n0 * Kp;
-    auto stage = [&](int k) __attribute__((always_inline)) {
-        const uint32_t base = lds_address(smem) + (k & 1) * kStage;
+    // The scales follow, a dword per row of A, then B, 64 rows per load (waves
+    // beyond those repeat one, so that every wave counts the same loads).
+    constexpr int kScaleBytes = E8M0 ? 1 : 4, kScaleLoads = (BM + BN) / 64;
+    const int sgroup = wave % kScaleLoads;
+    const bool of_a = sgroup * 64 < BM;
+    const Fp8Operand& so = of_a ? g.a : g.b;
+    const int64_t srows = of_a ? g.M : g.N, sfirst = of_a ? m0 : n0;
+    const int64_t sstep = (so.tile ? (srows + 127) / 128 : srows) * kScaleBytes;
+    const int64_t srow = min(sfirst + sgroup * 64 - (of_a ? 0 : BM) + lane, srows - 1);
+    const uint32_t os = (uint32_t)(so.tile ? (srow >> 7) - (sfirst >> 7) : srow - sfirst) * kScaleBytes;
+    const uint8_t* ts = (const uint8_t*)so.scales + (so.tile ? sfirst >> 7 : sfirst) * kScaleBytes;
+    auto stage = [&](int k, int buf) __attribute__((always_inline)) {
+        const uint32_t base = lds_address(smem) + buf * kStage;
         const uint8_t* ka = uniform(ta + (int64_t)k * 128);
         const uint8_t* kb = uniform(tb + (int64_t)k * 128);
 #pragma unroll
         for (int i = 0; i < LA; ++i) load_lds16(ka, oa[i], base + (wave * LA + i) * 1024);
 #pragma unroll
         for (int i = 0; i < LB; ++i) load_lds16(kb, ob[i], base + BM * 128 + (wave * LB + i) * 1024);
-    };
-
-    // ---- scales: thread t < BM + BN brings the scale of row t of A, then B,
-    // a block ahead, and leaves it in LDS where the lanes read theirs at once:
-    // A's as [16-row column c][tile i] of each wave row, B's by row (fp32) or
-    // like A's (hardware).
-    constexpr int kScaleBytes = E8M0 ? 1 : 4;
-    const uint8_t* sp = nullptr;
-    int64_t sstep = 0;
-    int sput = 0;
-    if (tid < BM) {
-        const int64_t m = min(m0 + tid, g.M - 1);
-        sstep = (g.a.tile ? (g.M + 127) / 128 : g.M) * kScaleBytes;
-        sp = (const uint8_t*)g.a.scales + (g.a.tile ? m >> 7 : m) * kScaleBytes;
-        sput = (tid / WM) * WM + (tid & 15) * MI + (tid % WM) / 16;
-    } else if (tid < BM + BN) {
-        const int r = tid - BM;
-        const int64_t n = min(n0 + r, g.N - 1);
-        sstep = (g.b.tile ? (g.N + 127) / 128 : g.N) * kScaleBytes;
-        sp = (const uint8_t*)g.b.scales + (g.b.tile ? n >> 7 : n) * kScaleBytes;
-        sput = SC == kHardware ? (r / WN) * WN + (r & 15) * NI + (r % WN) / 16 : r;
-        sput += BM;
-    }
-    uint32_t sreg = 0u;
-    auto load_scale = [&]() __attribute__((always_inline)) {
-        if (BM + BN >= kThreads || tid < BM + BN) {
-            if constexpr (E8M0) sreg = *sp;
-            else sreg = *(const uint32_t*)sp;
-            sp += sstep;
-        }
-    };
-    auto put_scale = [&](int k) __attribute__((always_inline)) {
-        if (BM + BN >= kThreads || tid < BM + BN) {
-            if constexpr (SC == kHardware) ((uint8_t*)scales)[(k & 1) * (BM + BN) + sput] = (uint8_t)sreg;
-            else scales[(k & 1) * (BM + BN) + sput] = E8M0 ? e8m0_value(sreg) : __uint_as_float(sreg);
-        }
+        load_lds_scale<E8M0>(uniform(ts + k * sstep), os, base + kCodes + sgroup * 256);
     };
 
     // ---- fragment reads: units 2q and 2q + 1 of row c (tile t: row 16 t + c)
@@ -205,43 +196,52 @@ __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
 #pragma unroll
         for (int i = 0; i < MI; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    if (nchunks > 0) {
-        stage(0);
-        load_scale();
-    }
+#pragma unroll
+    for (int k = 0; k < STAGES - 1; ++k)
+        if (k < nchunks) stage(k, k);
+    int buf = 0;
     for (int k = 0; k < nchunks; ++k) {
-        put_scale(k);
-        wait_staged();  // this wave's share of chunk k is in LDS
+        // this wave's share of chunk k is in LDS; up to STAGES - 2 later ones stay in flight
+        const int later = min(STAGES - 2, nchunks - 1 - k);
+        if (later == 0) wait_loads<0>();
+        else if (later == 1) wait_loads<kLoads>();
+        else wait_loads<2 * kLoads>();
+        static_assert(STAGES <= 4, "the waits above");
         __syncthreads();
-        if (k + 1 < nchunks) {
-            stage(k + 1);
-            load_scale();
-        }
-        const uint8_t* base = smem + (k & 1) * kStage;
-        const float* sc = scales + (k & 1) * (BM + BN);
+        // every wave has read chunk k - 1: its buffer takes chunk k + STAGES - 1
+        if (k + STAGES - 1 < nchunks) stage(k + STAGES - 1, buf == 0 ? STAGES - 1 : buf - 1);
+        const uint8_t* base = smem + buf * kStage;
+        const uint32_t* sc = reinterpret_cast<const uint32_t*>(base + kCodes);
+        buf = buf == STAGES - 1 ? 0 : buf + 1;
 
         Frag<EXACT, AE5> a[MI];
         Frag<EXACT, BE5> b[2];
         f32x4 part[2][MI], sv[2];
-        scales_a fa;
-        uint32_t xa = 0u;
-        u32x2 xb = {0u, 0u};
+        float fa[MI];
+        int xa[SC == kHardware ? MI : 1], xb[SC == kHardware ? NI : 1];
+        auto value = [&](uint32_t w) __attribute__((always_inline)) { return E8M0 ? e8m0_value(w & 0xFFu) : __uint_as_float(w); };
         if constexpr (SC == kHardware) {
-            const uint8_t* bytes = (const uint8_t*)scales + (k & 1) * (BM + BN);
-            if constexpr (MI == 4) xa = *reinterpret_cast<const uint32_t*>(bytes + wm * WM + c * MI);
-            else xa = *reinterpret_cast<const uint16_t*>(bytes + wm * WM + c * MI);
-            if constexpr (NI == 8) xb = *reinterpret_cast<const u32x2*>(bytes + BM + wn * WN + c * NI);
-            else xb.x = *reinterpret_cast<const uint32_t*>(bytes + BM + wn * WN + c * NI);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) xa[i] = (int)sc[wm * WM + 16 * i + c];
+#pragma unroll
+            for (int j = 0; j < NI; ++j) xb[j] = (int)sc[BM + wn * WN + 16 * j + c];
         } else {
-            fa = *reinterpret_cast<const scales_a*>(sc + wm * WM + c * MI);
-            if constexpr (SC == kTileB) fa *= sc[BM + wn * WN];
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                fa[i] = value(sc[wm * WM + 16 * i + c]);
+                if constexpr (SC == kTileB) fa[i] *= value(sc[BM + wn * WN]);
+            }
         }
         auto raw_b = [&](int j, i32x4& x, i32x4& y) __attribute__((always_inline)) {
             x = *reinterpret_cast<const i32x4*>(base + b_base + j * 2048 + o0);
             y = *reinterpret_cast<const i32x4*>(base + b_base + j * 2048 + o1);
         };
         auto read_sv = [&](int j) __attribute__((always_inline)) {
-            if constexpr (SC == kVectorB) sv[j & 1] = *reinterpret_cast<const f32x4*>(sc + BM + wn * WN + 4 * q + 16 * j);
+            if constexpr (SC == kVectorB) {
+                const u32x4 w = *reinterpret_cast<const u32x4*>(sc + BM + wn * WN + 4 * q + 16 * j);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sv[j & 1][e] = value(w[e]);
+            }
         };
         auto add_part = [&](int j, int i, const f32x4& p) __attribute__((always_inline)) {
 #pragma unroll
@@ -285,8 +285,8 @@ __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
 #pragma unroll
                 for (int i = 0; i < MI; ++i) {
                     if constexpr (SC == kHardware) {
-                        // byte i of xa, byte j of xb
-                        acc[j][i] = mfma_scaled<BE5, AE5>(j & 3, i, b[j & 1].v, a[i].v, acc[j][i], j < 4 ? xb.x : xb.y, xa);
+                        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j & 1].v, a[i].v, acc[j][i], BE5, AE5, 0,
+                                                                                     xb[j], 0, xa[i]);
                     } else {
                         f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
                         part[j & 1][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j & 1].v, a[i].v, z, BE5, AE5, 0, 0, 0, 0);
@@ -300,7 +300,7 @@ __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
             }
         }
         if constexpr (SC != kHardware && !EXACT) {
-            __builtin_amdgcn_sched_group_barrier(kSchedDs, 3 + 2 * MI + (SC == kVectorB), 0);
+            __builtin_amdgcn_sched_group_barrier(kSchedDs, 2 + 3 * MI + 1, 0);
 #pragma unroll
             for (int t = 0; t < NI * MI; ++t) {
                 __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
@@ -311,46 +311,146 @@ __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
     }
 
     // ---- epilogue: lane (c, q) holds columns n .. n + 3 of row m
-    const bool vec = g.N % 4 == 0;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
         const int64_t m = m0 + wm * WM + 16 * i + c;
         if (m >= g.M) continue;
 #pragma unroll
-        for (int j = 0; j < NI; ++j) {
-            const int64_t n = n0 + wn * WN + 16 * j + 4 * q;
-            const f32x4 v = acc[j][i];
-            if (vec) {
-                if (n >= g.N) continue;
-                if (g.c_bf16)
-                    *reinterpret_cast<bf16x4*>((__bf16*)g.c + m * g.N + n) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-                else
-                    *reinterpret_cast<f32x4*>((float*)g.c + m * g.N + n) = v;
+        for (int j = 0; j < NI; ++j) store4(g, m, n0 + wn * WN + 16 * j + 4 * q, acc[j][i]);
+    }
+}
+
+// Few rows of A: the time is that of reading B once.  A workgroup owns 16 rows
+// of B and all of A (MT tiles of 16 rows); its waves take every W-th block of K
+// straight from memory (no wave shares another's codes, so LDS would only add a
+// trip), several blocks in flight, and their sums meet in LDS in a fixed order.
+template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int W, int MT>
+__global__ __launch_bounds__(W * 64) void gemm_fp8_skinny_kernel(GemmFp8Args g) {
+    __shared__ __align__(16) f32x4 sums[W][MT][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, q = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t Kp = (g.K + 127) / 128 * 128;
+    const int nchunks = (int)(Kp / 128);
+    const int64_t as_step = g.a.tile ? (g.M + 127) / 128 : g.M, bs_step = g.b.tile ? (g.N + 127) / 128 : g.N;
+
+    const uint8_t* pb = g.b.codes + min(n0 + c, g.N - 1) * Kp + 32 * q;
+    const uint8_t* pa[MT];
+    int64_t as_at[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int64_t m = min((int64_t)(16 * i + c), g.M - 1);
+        pa[i] = g.a.codes + m * Kp + 32 * q;
+        as_at[i] = g.a.tile ? m >> 7 : m;
+    }
+    // this lane's rows of B: as an operand row (hardware scales), or as the
+    // four output columns 4 q .. 4 q + 3
+    int64_t bs_at[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int64_t n = min(n0 + (SC == kHardware ? c : 4 * q + e), g.N - 1);
+        bs_at[e] = SC == kTileB ? n0 >> 7 : g.b.tile ? n >> 7 : n;
+    }
+    auto scale_at = [&](const void* base, int64_t at) __attribute__((always_inline)) {
+        if constexpr (E8M0) return e8m0_value(((const uint8_t*)base)[at]);
+        else return ((const float*)base)[at];
+    };
+
+    f32x4 acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int kDepth = MT == 1 ? 4 : 2;  // blocks in flight
+    for (int k0 = wave; k0 < nchunks; k0 += W * kDepth) {
+        i32x4 bx[kDepth], by[kDepth], ax[kDepth][MT], ay[kDepth][MT];
+        float sa[kDepth][MT], sb[kDepth][4];
+        int ha[kDepth][MT], hb[kDepth];
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+            const int64_t k = min(k0 + d * W, nchunks - 1);  // past the end: read again, not used
+            bx[d] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pb + k * 128));
+            by[d] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pb + k * 128 + 16));
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                ax[d][i] = *reinterpret_cast<const i32x4*>(pa[i] + k * 128);
+                ay[d][i] = *reinterpret_cast<const i32x4*>(pa[i] + k * 128 + 16);
+                if constexpr (SC == kHardware) ha[d][i] = ((const uint8_t*)g.a.scales)[k * as_step + as_at[i]];
+                else sa[d][i] = scale_at(g.a.scales, k * as_step + as_at[i]);
+            }
+            if constexpr (SC == kHardware) {
+                hb[d] = ((const uint8_t*)g.b.scales)[k * bs_step + bs_at[0]];
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (n + e >= g.N) continue;
-                    if (g.c_bf16) ((__bf16*)g.c)[m * g.N + n + e] = (__bf16)v[e];
-                    else ((float*)g.c)[m * g.N + n + e] = v[e];
+                for (int e = 0; e < (SC == kTileB ? 1 : 4); ++e) sb[d][e] = scale_at(g.b.scales, k * bs_step + bs_at[e]);
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+            const bool used = k0 + d * W < nchunks;  // selected, not branched on: the loads stay ahead
+            Frag<EXACT, BE5> b;
+            b.set(bx[d], by[d]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                Frag<EXACT, AE5> a;
+                a.set(ax[d][i], ay[d][i]);
+                if constexpr (SC == kHardware) {
+                    const f32x4 z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, acc[i], BE5, AE5, 0, hb[d], 0, ha[d][i]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][e] = used ? z[e] : acc[i][e];
+                } else {
+                    f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if constexpr (EXACT) {
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) z = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.v[s], a.v[s], z, 0, 0, 0);
+                    } else {
+                        z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, z, BE5, AE5, 0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[i][e] = used ? __builtin_fmaf(z[e], sa[d][i] * sb[d][SC == kTileB ? 0 : e], acc[i][e]) : acc[i][e];
                 }
             }
         }
     }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sums[wave][i][lane] = acc[i];
+    __syncthreads();
+    // wave i stores tile i; waves behind the last tile are done
+    for (int i = wave; i < MT; i += W) {
+        f32x4 v = sums[0][i][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) v += sums[w][i][lane];
+        const int64_t m = 16 * i + c, n = n0 + 4 * q;
+        if (m < g.M) store4(g, m, n, v);
+    }
 }
 
-template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MW, int MI, int NI>
-void launch_tiled(const GemmFp8Args& g, hipStream_t stream) {
+template <int MW, int MI, int NI>
+int64_t tiles_of(const GemmFp8Args& g) {
     constexpr int BM = MW * 16 * MI, BN = 32 * NI;
-    const int64_t tiles = ((g.M + BM - 1) / BM) * ((g.N + BN - 1) / BN);
-    hipLaunchKernelGGL((gemm_fp8_kernel<EXACT, AE5, BE5, SC, E8M0, MW, MI, NI>), dim3((unsigned)tiles), dim3(MW * 128), 0,
-                       stream, g);
+    return ((g.M + BM - 1) / BM) * ((g.N + BN - 1) / BN);
+}
+
+template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MW, int MI, int NI, int STAGES>
+void launch_tiled(const GemmFp8Args& g, hipStream_t stream) {
+    hipLaunchKernelGGL((gemm_fp8_kernel<EXACT, AE5, BE5, SC, E8M0, MW, MI, NI, STAGES>), dim3((unsigned)tiles_of<MW, MI, NI>(g)),
+                       dim3(MW * 128), 0, stream, g);
+}
+
+template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MT>
+void launch_skinny(const GemmFp8Args& g, hipStream_t stream) {
+    constexpr int W = 8;
+    hipLaunchKernelGGL((gemm_fp8_skinny_kernel<EXACT, AE5, BE5, SC, E8M0, W, MT>), dim3((unsigned)((g.N + 15) / 16)),
+                       dim3(W * 64), 0, stream, g);
 }
 
 template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0>
 void launch_size(const GemmFp8Args& g, hipStream_t stream) {
-    const int64_t large = ((g.M + 255) / 256) * ((g.N + 255) / 256);
-    if (large >= 192 && !EXACT) launch_tiled<EXACT, AE5, BE5, SC, E8M0, 4, 4, 8>(g, stream);
-    else launch_tiled<EXACT, AE5, BE5, SC, E8M0, 2, 4, 4>(g, stream);
+    if (g.M <= 16) return launch_skinny<EXACT, AE5, BE5, SC, E8M0, 1>(g, stream);
+    if constexpr (!EXACT)
+        if (tiles_of<4, 4, 8>(g) >= 192) return launch_tiled<EXACT, AE5, BE5, SC, E8M0, 4, 4, 8, 2>(g, stream);
+    if (tiles_of<2, 4, 4>(g) >= 256) return launch_tiled<EXACT, AE5, BE5, SC, E8M0, 2, 4, 4, 2>(g, stream);
+    launch_tiled<EXACT, AE5, BE5, SC, E8M0, 2, 2, 2, 4>(g, stream);
 }
 
 template <bool EXACT, bool AE5, bool BE5, bool E8M0>

@@ -12,12 +12,11 @@ function launches on the device of its tensors, on torch's current stream of
 that device unless one is given.
 """
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
 
-from . import _check, _i64, _PKG, _ptr, _require, _require_scalar, _same_device
+from . import _check, _i64, _PKG, _require, _require_scalar, _same_device
 
 LAYER_LIB_PATH = os.path.join(_PKG, "libue5m3fp4_layer.so")
 
@@ -65,15 +64,32 @@ def _launch(where, device, stream, *args):
     import torch
 
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
     elif getattr(stream, "device", device) != device:
         raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors are on {device}")
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    fn = getattr(load_layer_library(), where)
-    guard = contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-    with guard:
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    fn = getattr(_lib or load_layer_library(), where)
+    if torch.cuda.current_device() == device.index:
         status = fn(*args, handle)
-    _check(status, where)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, handle)
+    if status != 0:
+        _check(status, where)
+
+
+def _device_of(where, *tensors):
+    """The device that all the tensors (or None) share."""
+    device = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != device:
+            _same_device(where, *tensors)
+    return device
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 def _blocks(n):
@@ -116,15 +132,17 @@ def _check_fp8(q, name):
         raise ValueError(f"{name}: unknown format {q.fmt}")
     if q.cols < 0:
         raise ValueError(f"{name}: cols is negative")
-    _require(q.codes, (torch.uint8,), f"{name} codes", 2, contiguous=True)
-    _require(q.scales, (torch.float32, torch.uint8), f"{name} scales", 2, contiguous=True)
-    rows, blocks = q.codes.shape[0], _blocks(q.cols)
-    if q.codes.shape[1] != blocks * FP8_BLOCK:
+    _require(q.codes, (torch.uint8,), name + " codes", 2, contiguous=True)
+    _require(q.scales, (torch.float32, torch.uint8), name + " scales", 2, contiguous=True)
+    rows, padded = q.codes.shape
+    blocks = _blocks(q.cols)
+    if padded != blocks * FP8_BLOCK:
         raise ValueError(f"{name}: codes {tuple(q.codes.shape)} do not match {q.cols} columns "
                          f"([{rows}][{blocks * FP8_BLOCK}])")
-    if tuple(q.scales.shape) != (blocks, _blocks(rows) if q.tile else rows):
+    if q.scales.shape != (blocks, _blocks(rows) if q.tile else rows):
         raise ValueError(f"{name}: scales {tuple(q.scales.shape)} do not match a {rows} x {q.cols} operand "
                          f"([{blocks}][{_blocks(rows) if q.tile else rows}])")
+    return rows
 
 
 def _matrix(t, name):
@@ -148,34 +166,32 @@ def quantize_fp8(x, row=None, col=None, stream=None):
     if not outs:
         raise ValueError("quantize_fp8: row or col is required")
     for o, n, r, c in outs:
-        _check_fp8(o, n)
-        if (o.rows, o.cols) != (r, c):
+        if (_check_fp8(o, n), o.cols) != (r, c):
             raise ValueError(f"{n} is a {o.rows} x {o.cols} operand, expected {r} x {c}")
     q = outs[0][0]
     if len(outs) == 2 and (row.fmt, row.tile, row.scales.dtype) != (col.fmt, col.tile, col.scales.dtype):
         raise ValueError("row and col disagree on format, tile mode or scale type")
-    _same_device("quantize_fp8", x, *(t for o, *_ in outs for t in (o.codes, o.scales)))
-    _launch("ue5m3fp4_quantize_fp8", x.device, stream, _ptr(x), rows, cols, ld, q.fmt,
-            int(q.scales.dtype == torch.uint8), int(q.tile), *(
-                _ptr(t) for o in (row, col) for t in ((o.codes, o.scales) if o is not None else (None, None))))
+    buffers = [t for o in (row, col) for t in ((o.codes, o.scales) if o is not None else (None, None))]
+    device = _device_of("quantize_fp8", x, *buffers)
+    _launch("ue5m3fp4_quantize_fp8", device, stream, x.data_ptr(), rows, cols, ld, q.fmt,
+            int(q.scales.dtype == torch.uint8), int(q.tile), *map(_address, buffers))
 
 
 def _gemm_fp8(a, b, out, stream, na, nb):
     import torch
 
-    _check_fp8(a, na)
-    _check_fp8(b, nb)
-    if a.cols != b.cols:
-        raise ValueError(f"{na} and {nb} disagree on the contraction axis ({a.cols} vs {b.cols})")
+    M, N, K = _check_fp8(a, na), _check_fp8(b, nb), a.cols
+    if K != b.cols:
+        raise ValueError(f"{na} and {nb} disagree on the contraction axis ({K} vs {b.cols})")
     if a.scales.dtype != b.scales.dtype:
         raise ValueError(f"{na} and {nb} have scales of different types")
     _require(out, (torch.float32, torch.bfloat16), "out", 2, contiguous=True)
-    if tuple(out.shape) != (a.rows, b.rows):
-        raise ValueError(f"output must be a contiguous [{a.rows}][{b.rows}] tensor")
-    _same_device("gemm_fp8", a.codes, a.scales, b.codes, b.scales, out)
-    _launch("ue5m3fp4_gemm_fp8_nt", out.device, stream, _ptr(a.codes), _ptr(a.scales), a.fmt, int(a.tile),
-            _ptr(b.codes), _ptr(b.scales), b.fmt, int(b.tile), int(a.scales.dtype == torch.uint8), a.rows, b.rows,
-            a.cols, _ptr(out), int(out.dtype == torch.float32))
+    if out.shape != (M, N):
+        raise ValueError(f"output must be a contiguous [{M}][{N}] tensor")
+    device = _device_of("gemm_fp8", out, a.codes, a.scales, b.codes, b.scales)
+    _launch("ue5m3fp4_gemm_fp8_nt", device, stream, a.codes.data_ptr(), a.scales.data_ptr(), a.fmt, int(a.tile),
+            b.codes.data_ptr(), b.scales.data_ptr(), b.fmt, int(b.tile), int(a.scales.dtype == torch.uint8), M, N, K,
+            out.data_ptr(), int(out.dtype == torch.float32))
     return out
 
 
@@ -199,10 +215,10 @@ def gemm_fp8_wgrad(dy_col, x_col, dw, stream=None):
     return _gemm_fp8(dy_col, x_col, dw, stream, "dy_col", "x_col")
 
 
-def _flat(t, name, shape):
-    """(row stride) of a tensor taken as a matrix of `shape` rows and columns."""
+def _flat(t, name, cols):
+    """Row stride of a tensor taken as a matrix of `cols` columns."""
     if t.is_contiguous():
-        return shape[1]
+        return cols
     if t.dim() != 2:
         raise ValueError(f"{name} must be contiguous, or a matrix with unit stride along its columns")
     return _matrix(t, name)[2]
@@ -214,26 +230,27 @@ def _dropout(where, x, p, seed, offset, out, residual, amax, stream, nx, nout):
     types = (torch.bfloat16, torch.float32)
     _require(x, types, nx)
     _require(out, types, nout)
-    if tuple(out.shape) != tuple(x.shape):
-        raise ValueError(f"{nout} has shape {tuple(out.shape)}, expected {tuple(x.shape)}")
+    shape = x.shape
+    if out.shape != shape:
+        raise ValueError(f"{nout} has shape {tuple(out.shape)}, expected {tuple(shape)}")
     if residual is not None:
         _require(residual, (out.dtype,), "residual")
-        if tuple(residual.shape) != tuple(x.shape):
-            raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {tuple(x.shape)}")
+        if residual.shape != shape:
+            raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {tuple(shape)}")
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p must lie in [0, 1] (got {p})")
     if not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 32:
         raise ValueError("seed must fit 64 unsigned bits and offset 32")
     if amax is not None:
         _require_scalar(amax, "amax")
-    _same_device("dropout", x, out, residual, amax)
-    shape = tuple(x.shape) if x.dim() == 2 else (1, x.numel())
+    device = _device_of("dropout", x, out, residual, amax)
+    rows, cols = shape if len(shape) == 2 else (1, x.numel())
     f32 = torch.float32
-    args = [_ptr(x), int(x.dtype == f32), _flat(x, nx, shape)]
+    args = [x.data_ptr(), int(x.dtype == f32), _flat(x, nx, cols)]
     if where == "ue5m3fp4_dropout":
-        args += [_ptr(residual), _flat(residual, "residual", shape) if residual is not None else 0]
-    _launch(where, x.device, stream, *args, _ptr(out), int(out.dtype == f32), _flat(out, nout, shape), *shape,
-            float(p), int(seed), int(offset), _ptr(amax))
+        args += [_address(residual), _flat(residual, "residual", cols) if residual is not None else 0]
+    _launch(where, device, stream, *args, out.data_ptr(), int(out.dtype == f32), _flat(out, nout, cols), rows, cols,
+            float(p), int(seed), int(offset), _address(amax))
     return out
 
 
