@@ -374,13 +374,14 @@ __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
     }
 }
 
-// Few rows of A: the time is that of reading B once.  A workgroup owns 16 rows
-// of B and all of A (MT tiles of 16 rows); its waves take every W-th block of K
-// straight from memory (no wave shares another's codes, so LDS would only add a
-// trip), several blocks in flight, and their sums meet in LDS in a fixed order.
-template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int W, int MT>
+// At most 16 rows of A: the time is that of reading B once.  A workgroup owns 16
+// rows of B and all of A; its waves take every W-th block of K straight from
+// memory (no wave shares another's codes, so LDS would only add a trip), four
+// blocks in flight, and their sums meet in LDS in a fixed order.
+template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int W>
 __global__ __launch_bounds__(W * 64) void gemm_fp8_skinny_kernel(GemmFp8Args g) {
-    __shared__ __align__(16) f32x4 sums[W][MT][64];
+    constexpr int kDepth = 4;
+    __shared__ __align__(16) f32x4 sums[W][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
@@ -389,94 +390,74 @@ __global__ __launch_bounds__(W * 64) void gemm_fp8_skinny_kernel(GemmFp8Args g) 
     const int nchunks = (int)(Kp / 128);
     const int64_t as_step = g.a.tile ? (g.M + 127) / 128 : g.M, bs_step = g.b.tile ? (g.N + 127) / 128 : g.N;
 
+    const int64_t m = min((int64_t)c, g.M - 1);
+    const uint8_t* pa = g.a.codes + m * Kp + 32 * q;
     const uint8_t* pb = g.b.codes + min(n0 + c, g.N - 1) * Kp + 32 * q;
-    const uint8_t* pa[MT];
-    int64_t as_at[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int64_t m = min((int64_t)(16 * i + c), g.M - 1);
-        pa[i] = g.a.codes + m * Kp + 32 * q;
-        as_at[i] = g.a.tile ? m >> 7 : m;
-    }
+    const int64_t as_at = g.a.tile ? 0 : m;
     // this lane's rows of B: as an operand row (hardware scales), or as the
     // four output columns 4 q .. 4 q + 3
-    int64_t bs_at[4];
+    constexpr int kSb = SC == kVectorB ? 4 : 1;
+    int64_t bs_at[kSb];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int64_t n = min(n0 + (SC == kHardware ? c : 4 * q + e), g.N - 1);
-        bs_at[e] = SC == kTileB ? n0 >> 7 : g.b.tile ? n >> 7 : n;
+    for (int e = 0; e < kSb; ++e) {
+        const int64_t n = min(n0 + (SC == kHardware ? c : SC == kTileB ? 0 : 4 * q + e), g.N - 1);
+        bs_at[e] = g.b.tile ? n >> 7 : n;
     }
     auto scale_at = [&](const void* base, int64_t at) __attribute__((always_inline)) {
         if constexpr (E8M0) return e8m0_value(((const uint8_t*)base)[at]);
         else return ((const float*)base)[at];
     };
 
-    f32x4 acc[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int kDepth = MT == 1 ? 4 : 2;  // blocks in flight
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int k0 = wave; k0 < nchunks; k0 += W * kDepth) {
-        i32x4 bx[kDepth], by[kDepth], ax[kDepth][MT], ay[kDepth][MT];
-        float sa[kDepth][MT], sb[kDepth][4];
-        int ha[kDepth][MT], hb[kDepth];
+        i32x4 bx[kDepth], by[kDepth], ax[kDepth], ay[kDepth];
+        float sa[kDepth], sb[kDepth][kSb];
+        int ha[kDepth], hb[kDepth];
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {
             const int64_t k = min(k0 + d * W, nchunks - 1);  // past the end: read again, not used
             bx[d] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pb + k * 128));
             by[d] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pb + k * 128 + 16));
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                ax[d][i] = *reinterpret_cast<const i32x4*>(pa[i] + k * 128);
-                ay[d][i] = *reinterpret_cast<const i32x4*>(pa[i] + k * 128 + 16);
-                if constexpr (SC == kHardware) ha[d][i] = ((const uint8_t*)g.a.scales)[k * as_step + as_at[i]];
-                else sa[d][i] = scale_at(g.a.scales, k * as_step + as_at[i]);
-            }
+            ax[d] = *reinterpret_cast<const i32x4*>(pa + k * 128);
+            ay[d] = *reinterpret_cast<const i32x4*>(pa + k * 128 + 16);
             if constexpr (SC == kHardware) {
+                ha[d] = ((const uint8_t*)g.a.scales)[k * as_step + as_at];
                 hb[d] = ((const uint8_t*)g.b.scales)[k * bs_step + bs_at[0]];
             } else {
+                sa[d] = scale_at(g.a.scales, k * as_step + as_at);
 #pragma unroll
-                for (int e = 0; e < (SC == kTileB ? 1 : 4); ++e) sb[d][e] = scale_at(g.b.scales, k * bs_step + bs_at[e]);
+                for (int e = 0; e < kSb; ++e) sb[d][e] = scale_at(g.b.scales, k * bs_step + bs_at[e]);
             }
         }
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {
             const bool used = k0 + d * W < nchunks;  // selected, not branched on: the loads stay ahead
+            Frag<EXACT, AE5> a;
             Frag<EXACT, BE5> b;
+            a.set(ax[d], ay[d]);
             b.set(bx[d], by[d]);
+            f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (SC == kHardware) {
+                z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, acc, BE5, AE5, 0, hb[d], 0, ha[d]);
+            } else if constexpr (EXACT) {
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                Frag<EXACT, AE5> a;
-                a.set(ax[d][i], ay[d][i]);
-                if constexpr (SC == kHardware) {
-                    const f32x4 z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, acc[i], BE5, AE5, 0, hb[d], 0, ha[d][i]);
+                for (int s = 0; s < 4; ++s) z = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.v[s], a.v[s], z, 0, 0, 0);
+            } else {
+                z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, z, BE5, AE5, 0, 0, 0, 0);
+            }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][e] = used ? z[e] : acc[i][e];
-                } else {
-                    f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if constexpr (EXACT) {
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) z = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.v[s], a.v[s], z, 0, 0, 0);
-                    } else {
-                        z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, z, BE5, AE5, 0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[i][e] = used ? __builtin_fmaf(z[e], sa[d][i] * sb[d][SC == kTileB ? 0 : e], acc[i][e]) : acc[i][e];
-                }
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (SC != kHardware) z[e] = __builtin_fmaf(z[e], sa[d] * sb[d][kSb == 4 ? e : 0], acc[e]);
+                acc[e] = used ? z[e] : acc[e];
             }
         }
     }
-#pragma unroll
-    for (int i = 0; i < MT; ++i) sums[wave][i][lane] = acc[i];
+    sums[wave][lane] = acc;
     __syncthreads();
-    // wave i stores tile i; waves behind the last tile are done
-    for (int i = wave; i < MT; i += W) {
-        f32x4 v = sums[0][i][lane];
+    if (wave > 0) return;
 #pragma unroll
-        for (int w = 1; w < W; ++w) v += sums[w][i][lane];
-        const int64_t m = 16 * i + c, n = n0 + 4 * q;
-        if (m < g.M) store4(g, m, n, v);
-    }
+    for (int w = 1; w < W; ++w) acc += sums[w][lane];
+    if (c < g.M) store4(g, c, n0 + 4 * q, acc);
 }
 
 template <int MW, int MI, int NI>
@@ -491,19 +472,34 @@ void launch_tiled(const GemmFp8Args& g, hipStream_t stream) {
                        dim3(MW * 128), 0, stream, g);
 }
 
-template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MT>
+template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0>
 void launch_skinny(const GemmFp8Args& g, hipStream_t stream) {
     constexpr int W = 8;
-    hipLaunchKernelGGL((gemm_fp8_skinny_kernel<EXACT, AE5, BE5, SC, E8M0, W, MT>), dim3((unsigned)((g.N + 15) / 16)),
+    hipLaunchKernelGGL((gemm_fp8_skinny_kernel<EXACT, AE5, BE5, SC, E8M0, W>), dim3((unsigned)((g.N + 15) / 16)),
                        dim3(W * 64), 0, stream, g);
 }
 
+// The tile size is the one whose rounds of workgroups take the least time, by
+// the time of a round over 4096 elements of K (us, measured; 256 CUs):
+//                        bf16 results   fp32 results
+//   64 x 64, 2 per CU          18             23
+//   128 x 128, 1 per CU        26             39
+//   128 x 128, 2 per CU        35             65
+//   256 x 256, 1 per CU        65              -
+// 512 x 4096 x 4096: 18.6 us against 22 in 128 x 128 tiles; 1024 x 4096 x 4096:
+// 26 against 35 in 64 x 64; 4096 x 4096 x 4096: 65 against 78 in 128 x 128.  At
+// most 16 rows of A go to the few-row kernel where the small tiles would leave
+// CUs idle (4096 outputs: 1 x 16384 20 us against 65; 16384 outputs: both 15).
 template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0>
 void launch_size(const GemmFp8Args& g, hipStream_t stream) {
-    if (g.M <= 16) return launch_skinny<EXACT, AE5, BE5, SC, E8M0, 1>(g, stream);
+    const int64_t small = tiles_of<2, 2, 2>(g), medium = tiles_of<2, 4, 4>(g), large = tiles_of<4, 4, 8>(g);
+    if (g.M <= 16 && small < 256) return launch_skinny<EXACT, AE5, BE5, SC, E8M0>(g, stream);
+    const int64_t t_small = (small + 511) / 512 * (EXACT ? 23 : 18);
+    const int64_t t_medium = medium <= 256 ? (EXACT ? 39 : 26) : (medium + 511) / 512 * (EXACT ? 65 : 35);
     if constexpr (!EXACT)
-        if (tiles_of<4, 4, 8>(g) >= 192) return launch_tiled<EXACT, AE5, BE5, SC, E8M0, 4, 4, 8, 2>(g, stream);
-    if (tiles_of<2, 4, 4>(g) >= 256) return launch_tiled<EXACT, AE5, BE5, SC, E8M0, 2, 4, 4, 2>(g, stream);
+        if ((large + 255) / 256 * 65 <= min(t_small, t_medium))
+            return launch_tiled<EXACT, AE5, BE5, SC, E8M0, 4, 4, 8, 2>(g, stream);
+    if (t_medium <= t_small) return launch_tiled<EXACT, AE5, BE5, SC, E8M0, 2, 4, 4, 2>(g, stream);
     launch_tiled<EXACT, AE5, BE5, SC, E8M0, 2, 2, 2, 4>(g, stream);
 }
 
