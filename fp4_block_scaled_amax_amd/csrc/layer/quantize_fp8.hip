@@ -12,7 +12,21 @@
 //    The amaxes of the 8 rows meet there (two rows per packed 16-bit max),
 //    lane u computes the scale of row u % 8 and broadcasts it.
 //  - Transposed pass, through LDS (XOR-swizzled, conflict-free): a lane quad
-//    owns a column pair, each lane 32 of its 128 rows.
+//    owns a column pair, each lane 16 rows of either half, so that the quad's
+//    stores run over 64 contiguous bytes.
+//  - Tile order: bands of 4 tile rows, walked column by column: the tiles in
+//    flight then write runs of 512 bytes of each column of the transposed codes.
+//    Row by row the 8192 x 16384 case below takes 115 us, in bands of 16 rows
+//    122; a contiguous range per XCD loses 5-10 % (the outputs are whole lines,
+//    so no two tiles share one that an L2 would have to merge).
+//  - Cache policy: x is read once and the row-wise codes leave as whole lines per
+//    store, both non-temporal; the transposed codes leave as two stores of half a
+//    line and have to meet in L2 (non-temporal: 120 instead of 115 us).
+//
+// Bound: HBM.  Both outputs, inputs and outputs rotated past the 256 MB cache:
+// 8192 x 4096 28 us (4.9 TB/s), 8192 x 16384 110 us (4.9), 16384 x 4096 in tiles
+// 47 us (5.7); a plain copy of these sizes runs at 5.2 to 5.9.  Without the
+// divisions, or without the scale stores, the times are the same within 2 %.
 #include "../formats.hpp"
 #include "layer.hpp"
 
@@ -22,6 +36,7 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kThreads = 256;
+constexpr uint32_t kBand = 4;
 
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -106,9 +121,12 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_kernel(QuantizeFp8Args 
     __shared__ uint32_t wave_max[kThreads / 64];
     const int t = threadIdx.x, u = t & 15, rb = t >> 4;
     const uint32_t tiles_c = (uint32_t)((a.cols + kTile - 1) / kTile);
-    const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x % tiles_c;
+    const uint32_t tiles_r = (uint32_t)((a.rows + kTile - 1) / kTile);
+    const uint32_t band = blockIdx.x / (kBand * tiles_c), rem = blockIdx.x - band * kBand * tiles_c;
+    const uint32_t height = min(kBand, tiles_r - kBand * band);
+    const int64_t tr = kBand * band + rem % height, tc = rem / height;
     const int64_t R0 = tr * kTile, C0 = tc * kTile, c0 = C0 + 8 * u;
-    const int64_t Cp = (int64_t)tiles_c * kTile, Rp = (a.rows + kTile - 1) / kTile * kTile;
+    const int64_t Cp = (int64_t)tiles_c * kTile, Rp = (int64_t)tiles_r * kTile;
 
     u32x4 w[8];
     if (R0 + kTile <= a.rows && C0 + kTile <= a.cols && a.ld % 8 == 0) {
@@ -147,13 +165,12 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_kernel(QuantizeFp8Args 
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int row = rb + 16 * k;
-            *reinterpret_cast<u32x4*>(tile + row * (kTile * 2) + ((u ^ ((row >> 5) << 2)) << 4)) = w[k];
+            *reinterpret_cast<u32x4*>(tile + row * (kTile * 2) + ((u ^ (((row >> 4) & 3) << 2)) << 4)) = w[k];
         }
     }
     if (TILE || COL) __syncthreads();
     if (TILE) {
         ts = block_scale<E5M2, E8M0>(max(max(wave_max[0], wave_max[1]), max(wave_max[2], wave_max[3])));
-        const int64_t tiles_r = Rp / kTile;
         if (t == 0) {
             if (ROW) put_scale<E8M0>(a.row_scales, tc * tiles_r + tr, ts);
             if (COL) put_scale<E8M0>(a.col_scales, tr * (int64_t)tiles_c + tc, ts);
@@ -200,12 +217,13 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_kernel(QuantizeFp8Args 
     }
 
     if (COL) {
-        const int seg = t & 3, cp = t >> 2;  // 32 rows, column pair
+        const int seg = t & 3, cp = t >> 2;  // rows 16 seg .. + 15 of either half, column pair
         const int64_t ca = C0 + 2 * cp;
         uint32_t v[32];
-        const uint8_t* src = tile + seg * 32 * (kTile * 2) + (((cp >> 2) ^ (seg << 2)) << 4) + 4 * (cp & 3);
+        const uint8_t* src = tile + seg * 16 * (kTile * 2) + (((cp >> 2) ^ (seg << 2)) << 4) + 4 * (cp & 3);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = *reinterpret_cast<const uint32_t*>(src + i * (kTile * 2));
+        for (int i = 0; i < 32; ++i)
+            v[i] = *reinterpret_cast<const uint32_t*>(src + (i < 16 ? i : i + 48) * (kTile * 2));
         float ra, rb2;
         uint32_t ma, mb;
         if (TILE) {
@@ -227,7 +245,7 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_kernel(QuantizeFp8Args 
             ma = (seg & 1) ? omask : mine.mask;
             mb = (seg & 1) ? mine.mask : omask;
         }
-        uint8_t* dst = a.col_codes + ca * Rp + R0 + 32 * seg;
+        uint8_t* dst = a.col_codes + ca * Rp + R0 + 16 * seg;
         u32x4 o[2];
         if (ca < a.cols) {
 #pragma unroll
@@ -235,7 +253,7 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_kernel(QuantizeFp8Args 
                 o[i >> 2][i & 3] = ma & encode4<E5M2>(bf16_lo(v[4 * i]) * ra, bf16_lo(v[4 * i + 1]) * ra,
                                                       bf16_lo(v[4 * i + 2]) * ra, bf16_lo(v[4 * i + 3]) * ra);
             *reinterpret_cast<u32x4*>(dst) = o[0];
-            *reinterpret_cast<u32x4*>(dst + 16) = o[1];
+            *reinterpret_cast<u32x4*>(dst + 64) = o[1];
         }
         if (ca + 1 < a.cols) {
 #pragma unroll
@@ -243,7 +261,7 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_kernel(QuantizeFp8Args 
                 o[i >> 2][i & 3] = mb & encode4<E5M2>(bf16_hi(v[4 * i]) * rb2, bf16_hi(v[4 * i + 1]) * rb2,
                                                       bf16_hi(v[4 * i + 2]) * rb2, bf16_hi(v[4 * i + 3]) * rb2);
             *reinterpret_cast<u32x4*>(dst + Rp) = o[0];
-            *reinterpret_cast<u32x4*>(dst + Rp + 16) = o[1];
+            *reinterpret_cast<u32x4*>(dst + Rp + 64) = o[1];
         }
     }
 }
