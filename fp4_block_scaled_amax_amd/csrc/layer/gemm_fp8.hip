@@ -128,15 +128,17 @@ __device__ __forceinline__ void store4(const GemmFp8Args& g, int64_t m, int64_t 
     }
 }
 
-template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MW, int MI, int NI, int STAGES>
-__global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
+template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MW, int MI, int NI, int STAGES, int KG>
+__global__ __launch_bounds__(MW * 128 * KG, 2) void gemm_fp8_kernel(GemmFp8Args g) {
     static_assert(SC != kHardware || (E8M0 && !EXACT), "hardware scales are E8M0 bytes of the 8-bit instruction");
     constexpr int WM = 16 * MI, WN = 16 * NI, BM = MW * WM, BN = 2 * WN;
     constexpr int kCodes = (BM + BN) * 128, kStage = kCodes + (BM + BN) * 4;
-    __shared__ __align__(1024) uint8_t smem[STAGES * kStage];
+    __shared__ __align__(1024) uint8_t smem_all[KG * STAGES * kStage];
 
     const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int group = KG > 1 ? __builtin_amdgcn_readfirstlane(tid / (MW * 128)) : 0;
+    const int wave = __builtin_amdgcn_readfirstlane(KG > 1 ? (tid >> 6) % (MW * 2) : tid >> 6);
+    uint8_t* smem = smem_all + group * (STAGES * kStage);
     const int wm = wave >> 1, wn = wave & 1;
     const int c = lane & 15, q = lane >> 4;
 
@@ -144,7 +146,9 @@ __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
     tile_of((int)((g.M + BM - 1) / BM), (int)((g.N + BN - 1) / BN), tm, tn);
     const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
     const int64_t Kp = (g.K + 127) / 128 * 128;
-    const int nchunks = (int)(Kp / 128);
+    // group g of KG takes blocks g, g + KG, ...; every group makes the same turns
+    const int blocks = (int)(Kp / 128), turns = (blocks + KG - 1) / KG;
+    const int nchunks = (blocks - group + KG - 1) / KG;
 
     // ---- staging: one 1 KB load to LDS covers 8 rows x 128 codes; lane (r, p)
     // = (lane / 8, lane % 8) brings 16-byte unit p ^ (row / 2 % 8) of its row,
@@ -177,13 +181,14 @@ __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
     const uint8_t* ts = (const uint8_t*)so.scales + (so.tile ? sfirst >> 7 : sfirst) * kScaleBytes;
     auto stage = [&](int k, int buf) __attribute__((always_inline)) {
         const uint32_t base = lds_address(smem) + buf * kStage;
-        const uint8_t* ka = uniform(ta + (int64_t)k * 128);
-        const uint8_t* kb = uniform(tb + (int64_t)k * 128);
+        const int64_t kblock = (int64_t)k * KG + group;
+        const uint8_t* ka = uniform(ta + kblock * 128);
+        const uint8_t* kb = uniform(tb + kblock * 128);
 #pragma unroll
         for (int i = 0; i < LA; ++i) load_lds16(ka, oa[i], base + (wave * LA + i) * 1024);
 #pragma unroll
         for (int i = 0; i < LB; ++i) load_lds16(kb, ob[i], base + BM * 128 + (wave * LB + i) * 1024);
-        load_lds_scale<E8M0>(uniform(ts + k * sstep), os, base + kCodes + sgroup * 256);
+        load_lds_scale<E8M0>(uniform(ts + kblock * sstep), os, base + kCodes + sgroup * 256);
     };
 
     // ---- fragment reads: units 2q and 2q + 1 of row c (tile t: row 16 t + c)
@@ -215,7 +220,7 @@ __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
     f32x4 part[EXACT ? 1 : 2][EXACT ? 2 : MI], sv[2];
     float fa[MI], fa_next[MI];
     int xa[SC == kHardware ? MI : 1], xb[SC == kHardware ? NI : 1];
-    int xa_next[SC == kHardware ? MI : 1], xb_next[SC == kHardware ? NI : 1];
+    int xa_next[SC == kHardware ? MI : 1], xb_next = 0;
     i32x4 x, y;
 
     auto read_scales = [&](const uint32_t* sc) __attribute__((always_inline)) {
@@ -223,7 +228,8 @@ __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
 #pragma unroll
             for (int i = 0; i < MI; ++i) xa_next[i] = (int)sc[wm * WM + 16 * i + c];
 #pragma unroll
-            for (int j = 0; j < NI; ++j) xb_next[j] = (int)sc[BM + wn * WN + 16 * j + c];
+            for (int j = 0; j < NI - 1; ++j) xb[j] = (int)sc[BM + wn * WN + 16 * j + c];
+            xb_next = (int)sc[BM + wn * WN + 16 * (NI - 1) + c];  // the last column still needs its own
         } else {
             const float sb = SC == kTileB ? value(sc[BM + wn * WN]) : 1.0f;
 #pragma unroll
@@ -237,8 +243,7 @@ __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
         if constexpr (SC == kHardware) {
 #pragma unroll
             for (int i = 0; i < MI; ++i) xa[i] = xa_next[i];
-#pragma unroll
-            for (int j = 0; j < NI; ++j) xb[j] = xb_next[j];
+            xb[NI - 1] = xb_next;
         } else {
 #pragma unroll
             for (int i = 0; i < MI; ++i) fa[i] = fa_next[i];
@@ -271,13 +276,11 @@ __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
             }
         }
     };
-    // this wave's share of chunk k is in LDS; later ones, up to STAGES - 1, stay in flight
+    // this wave's share of chunk k is in LDS; of STAGES = 3 the next one stays in flight
     auto wait_chunk = [&](int k) __attribute__((always_inline)) {
-        const int later = min(STAGES - 2, nchunks - 1 - k);
-        if (later <= 0) wait_loads<0>();
-        else if (later == 1) wait_loads<kLoads>();
-        else wait_loads<2 * kLoads>();
-        static_assert(STAGES <= 4, "the waits above");
+        static_assert(STAGES == 2 || STAGES == 3, "at most one later block is in flight");
+        if (STAGES == 3 && k + 1 < nchunks) wait_loads<kLoads>();
+        else wait_loads<0>();
     };
 
     auto read_first = [&](const uint8_t* base) __attribute__((always_inline)) {
@@ -294,14 +297,18 @@ __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
 #pragma unroll
     for (int k = 0; k < STAGES - 1; ++k)
         if (k < nchunks) stage(k, k);
-    if (kLate && nchunks > 0) {
-        wait_chunk(0);
+    if (kLate && turns > 0) {
+        if (nchunks > 0) wait_chunk(0);
         __syncthreads();
         if (STAGES - 1 < nchunks) stage(STAGES - 1, STAGES - 1);
         read_first(smem);
     }
     int buf = 0;
-    for (int k = 0; k < nchunks; ++k) {
+    for (int k = 0; k < turns; ++k) {
+        if (KG > 1 && k >= nchunks) {  // the last turn of a group without a block: only its barrier
+            __syncthreads();
+            break;
+        }
         const uint8_t* base = smem + buf * kStage;
         const uint32_t* sc = reinterpret_cast<const uint32_t*>(base + kCodes);
         if constexpr (!kLate) {
@@ -332,14 +339,12 @@ __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
         }
         buf = buf == STAGES - 1 ? 0 : buf + 1;
         if constexpr (kLate) {
-            if constexpr (SC != kHardware) {
-                // the sums up to here stay on this side of the barrier (left to
-                // itself the compiler sinks them past it, and holds every part)
+            // the sums up to here stay on this side of the barrier (left to itself
+            // the compiler sinks them past it, and holds all they are made of)
 #pragma unroll
-                for (int j = 0; j < NI - 2; ++j)
+            for (int j = 0; j < (SC == kHardware ? NI - 1 : NI - 2); ++j)
 #pragma unroll
-                    for (int i = 0; i < MI; ++i) asm volatile("" : "+v"(acc[j][i]));
-            }
+                for (int i = 0; i < MI; ++i) asm volatile("" : "+v"(acc[j][i]));
             // every read of chunk k is done: its buffer takes chunk k + STAGES
             if (k + 1 < nchunks) wait_chunk(k + 1);
             __syncthreads();
@@ -362,6 +367,24 @@ __global__ __launch_bounds__(MW * 128, 2) void gemm_fp8_kernel(GemmFp8Args g) {
         } else {
             add_part(NI - 1, MI - 1);
         }
+    }
+
+    if constexpr (KG > 1) {
+        // the groups' sums meet in LDS, in the groups' order
+        static_assert(NI * MI * 16 * MW * 128 * (KG - 1) <= KG * STAGES * kStage, "the sums fit the buffers");
+        __syncthreads();
+        f32x4* sums = reinterpret_cast<f32x4*>(smem_all) + (wave * 64 + lane);
+        constexpr int kStep = MW * 128;
+        if (group > 0) {
+#pragma unroll
+            for (int t = 0; t < NI * MI; ++t) sums[((group - 1) * NI * MI + t) * kStep] = acc[t / MI][t % MI];
+        }
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int g2 = 0; g2 < KG - 1; ++g2)
+#pragma unroll
+            for (int t = 0; t < NI * MI; ++t) acc[t / MI][t % MI] += sums[(g2 * NI * MI + t) * kStep];
     }
 
     // ---- epilogue: lane (c, q) holds columns n .. n + 3 of row m
@@ -466,10 +489,10 @@ int64_t tiles_of(const GemmFp8Args& g) {
     return ((g.M + BM - 1) / BM) * ((g.N + BN - 1) / BN);
 }
 
-template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MW, int MI, int NI, int STAGES>
+template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MW, int MI, int NI, int STAGES, int KG>
 void launch_tiled(const GemmFp8Args& g, hipStream_t stream) {
-    hipLaunchKernelGGL((gemm_fp8_kernel<EXACT, AE5, BE5, SC, E8M0, MW, MI, NI, STAGES>), dim3((unsigned)tiles_of<MW, MI, NI>(g)),
-                       dim3(MW * 128), 0, stream, g);
+    hipLaunchKernelGGL((gemm_fp8_kernel<EXACT, AE5, BE5, SC, E8M0, MW, MI, NI, STAGES, KG>), dim3((unsigned)tiles_of<MW, MI, NI>(g)),
+                       dim3(MW * 128 * KG), 0, stream, g);
 }
 
 template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0>
@@ -481,26 +504,34 @@ void launch_skinny(const GemmFp8Args& g, hipStream_t stream) {
 
 // The tile size is the one whose rounds of workgroups take the least time, by
 // the time of a round over 4096 elements of K (us, measured; 256 CUs):
-//                        bf16 results   fp32 results
-//   64 x 64, 2 per CU          18             23
-//   128 x 128, 1 per CU        26             39
-//   128 x 128, 2 per CU        35             65
-//   256 x 256, 1 per CU        65              -
-// 512 x 4096 x 4096: 18.6 us against 22 in 128 x 128 tiles; 1024 x 4096 x 4096:
-// 26 against 35 in 64 x 64; 4096 x 4096 x 4096: 65 against 78 in 128 x 128.  At
-// most 16 rows of A go to the few-row kernel where the small tiles would leave
-// CUs idle (4096 outputs: 1 x 16384 20 us against 65; 16384 outputs: both 15).
+//                                              bf16 results   fp32 results
+//   64 x 64, 1 per CU, K in 2 or 4 groups           12             13
+//   64 x 64, 2 per CU, K in 2 groups                17             23
+//   128 x 128, 1 per CU, K in 2 groups              26             36
+//   128 x 128, 2 per CU                             35             65
+//   256 x 256, 1 per CU                             65              -
+// 512 x 4096 x 4096: 16.5 us, in 128 x 128 tiles 25; 1024 x 4096 x 4096: 26, in
+// 64 x 64 32; 4096 x 4096 x 4096: 65, in 128 x 128 78.  K in groups: 1024 x 1024
+// x 8192 (fp32) 25 us in 4 groups, 29 in 2, 36 in 1; 2048 x 2048 x 8192 72 in 2,
+// 79 in 1; a bf16 row by 16384 x 4096 is bound by memory and best at 2 groups of
+// 3 stages: 12.1, against 14.1 in 4 groups of 2.  At most 16 rows of A go to the
+// few-row kernel where small tiles would leave CUs idle (1 x 4096 x 16384: 20 us
+// against 41).
 template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0>
 void launch_size(const GemmFp8Args& g, hipStream_t stream) {
     const int64_t small = tiles_of<2, 2, 2>(g), medium = tiles_of<2, 4, 4>(g), large = tiles_of<4, 4, 8>(g);
     if (g.M <= 16 && small < 256) return launch_skinny<EXACT, AE5, BE5, SC, E8M0>(g, stream);
-    const int64_t t_small = (small + 511) / 512 * (EXACT ? 23 : 18);
-    const int64_t t_medium = medium <= 256 ? (EXACT ? 39 : 26) : (medium + 511) / 512 * (EXACT ? 65 : 35);
+    const int64_t t_small = small <= 256 ? (EXACT ? 13 : 12) : (small + 511) / 512 * (EXACT ? 23 : 17);
+    const int64_t t_medium = medium <= 256 ? (EXACT ? 36 : 26) : (medium + 511) / 512 * (EXACT ? 65 : 35);
     if constexpr (!EXACT)
         if ((large + 255) / 256 * 65 <= min(t_small, t_medium))
-            return launch_tiled<EXACT, AE5, BE5, SC, E8M0, 4, 4, 8, 2>(g, stream);
-    if (t_medium <= t_small) return launch_tiled<EXACT, AE5, BE5, SC, E8M0, 2, 4, 4, 2>(g, stream);
-    launch_tiled<EXACT, AE5, BE5, SC, E8M0, 2, 2, 2, 4>(g, stream);
+            return launch_tiled<EXACT, AE5, BE5, SC, E8M0, 4, 4, 8, 2, 1>(g, stream);
+    if (t_medium <= t_small) {
+        if (medium <= 256) return launch_tiled<EXACT, AE5, BE5, SC, E8M0, 2, 4, 4, 2, 2>(g, stream);
+        return launch_tiled<EXACT, AE5, BE5, SC, E8M0, 2, 4, 4, 2, 1>(g, stream);
+    }
+    if (small > 256) return launch_tiled<EXACT, AE5, BE5, SC, E8M0, 2, 2, 2, 2, 2>(g, stream);
+    launch_tiled<EXACT, AE5, BE5, SC, E8M0, 2, 2, 2, EXACT ? 2 : 3, EXACT ? 4 : 2>(g, stream);
 }
 
 template <bool EXACT, bool AE5, bool BE5, bool E8M0>
