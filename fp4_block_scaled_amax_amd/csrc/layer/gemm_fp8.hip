@@ -151,20 +151,20 @@ __global__ __launch_bounds__(MW * 128 * KG, 2) void gemm_fp8_kernel(GemmFp8Args 
     const int nchunks = (blocks - group + KG - 1) / KG;
 
     // ---- staging: one 1 KB load to LDS covers 8 rows x 128 codes; lane (r, p)
-    // = (lane / 8, lane % 8) brings 16-byte unit p ^ (row / 2 % 8) of its row,
-    // so that 16 rows' reads of one unit touch every bank once.  Offsets from
-    // the tile's first code fit 32 bits (K < 2^24).
+    // = (lane / 8, lane % 8) brings 16-byte unit p ^ r of its row, so that 8 rows'
+    // reads of one unit touch each of 32 banks once (16-byte reads go 8 lanes at
+    // a time).  Offsets from the tile's first code fit 32 bits (K < 2^24).
     constexpr int LA = BM / (16 * MW), LB = BN / (16 * MW), kLoads = LA + LB + 1;
     uint32_t oa[LA], ob[LB];
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
         const int row = (wave * LA + i) * 8 + (lane >> 3);
-        oa[i] = (uint32_t)min((int64_t)row, g.M - 1 - m0) * (uint32_t)Kp + 16 * ((lane & 7) ^ ((row >> 1) & 7));
+        oa[i] = (uint32_t)min((int64_t)row, g.M - 1 - m0) * (uint32_t)Kp + 16 * ((lane & 7) ^ (lane >> 3));
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
         const int row = (wave * LB + i) * 8 + (lane >> 3);
-        ob[i] = (uint32_t)min((int64_t)row, g.N - 1 - n0) * (uint32_t)Kp + 16 * ((lane & 7) ^ ((row >> 1) & 7));
+        ob[i] = (uint32_t)min((int64_t)row, g.N - 1 - n0) * (uint32_t)Kp + 16 * ((lane & 7) ^ (lane >> 3));
     }
     const uint8_t* ta = g.a.codes + m0 * Kp;
     const uint8_t* tb = g.b.codes + n0 * Kp;
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(MW * 128 * KG, 2) void gemm_fp8_kernel(GemmFp8Args 
     };
 
     // ---- fragment reads: units 2q and 2q + 1 of row c (tile t: row 16 t + c)
-    const int o0 = c * 128 + (((2 * q) ^ (c >> 1)) << 4), o1 = o0 ^ 16;
+    const int o0 = c * 128 + (((2 * q) ^ (c & 7)) << 4), o1 = o0 ^ 16;
     const int a_base = wm * WM * 128, b_base = BM * 128 + wn * WN * 128;
 
     f32x4 acc[NI][MI];
