@@ -65,6 +65,7 @@ int ue5m3fp4_quantize_fp8(const uint16_t* x, int64_t rows, int64_t cols, int64_t
     if ((row_codes == nullptr) != (row_scales == nullptr) || (col_codes == nullptr) != (col_scales == nullptr))
         return UE5M3FP4_EINVAL;
     if (!row_codes && !col_codes) return UE5M3FP4_EINVAL;  // no output requested
+    if (row_codes == col_codes || row_scales == col_scales) return UE5M3FP4_EINVAL;  // one buffer for both
     if (ld < cols) return UE5M3FP4_ESHAPE;
     if (!aligned16(x) || !aligned16(row_codes) || !aligned16(row_scales) || !aligned16(col_codes) ||
         !aligned16(col_scales))

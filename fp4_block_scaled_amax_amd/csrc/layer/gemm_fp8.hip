@@ -1,6 +1,40 @@
 // 8-bit "NT" GEMM with one scale per block of 128 along K:
 //   C[i][j] = sum_kb sA(i, kb) sB(j, kb) sum_{k in block kb} A(i, k) B(j, k)
 // with E4M3 / E5M2 codes and fp32 or E8M0 scales (include/ue5m3fp4_layer.h).
+//
+// Two arithmetics, by the type of the result.
+//  - bf16: v_mfma_f32_16x16x128_f8f6f4, one instruction per tile and block.  Of
+//    each 8 consecutive products it keeps what lies within 2^-13 of the largest
+//    (measured with single products added to a cancelling pair); across those
+//    groups it sums in fp32.  On random operands that is 2e-5 to 4e-5 of the
+//    result's norm, against 2e-3 for the rounding to bf16 that follows.
+//  - fp32: the codes widened to fp16, which holds every E4M3 and E5M2 value, and
+//    v_mfma_f32_16x16x32_f16: exact products, fp32 sums (1e-7), at half the rate.
+//    All 8-bit matrix instructions share the 13 bits, so no other one would do.
+// Either way a block's sum enters the fp32 accumulators by one FMA per element
+// with the block's scales; E8M0 scales of bf16 results are operands of the matrix
+// instruction instead, and nothing is left to the vector ALU.
+//
+// The operands are exchanged (B first), so that a lane's scale of A is one value
+// per tile and the four results it holds are four neighbouring columns of C: lane
+// (c, q) = (lane % 16, lane / 16) supplies 32 codes of row c of each operand and
+// holds columns 4 q .. 4 q + 3 of row c.  Which 32 of a row's 128 codes it has
+// does not matter as long as both operands agree: they share the block's scale.
+//
+// Codes go from memory straight to LDS, a block (128 of K) ahead of the one that
+// is multiplied; each wave multiplies MI x NI tiles.  launch_size() picks the
+// workgroup's tile.
+//
+// Measured (cold operands, TFLOP/s of 2 M N K; the card's library runs 2970 in
+// 8 bits with one scale per tensor and 1540 in fp16):
+//   8192 x 16384 x 4096, bf16, fp32 scales    545 us  2020  MFMA busy 0.47 at
+//       1.87 GHz; 0.38 of the cycles go to vector ALU work (4 FMAs per MFMA and
+//       lane), 0.34 of the waves' to waiting at the issue
+//   8192 x 4096 x 16384, bf16, E8M0 scales    440 us  2500  MFMA busy 0.55 at
+//       1.95 GHz, vector ALU 0.20
+//   4096 x 4096 x 8192, fp32, 1-D scales      262 us  1050  bound by the vector
+//       ALU (0.59 busy: 2 conversions, 2 multiplications and FMAs per MFMA)
+//   1 x 16384 x 4096, bf16                     12.1 us  5.5 TB/s of B
 #include "layer.hpp"
 
 namespace ue5m3fp4 {
@@ -15,8 +49,7 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kGroupM = 4;
-constexpr int kSchedMfma = 0x008, kSchedValu = 0x002, kSchedDs = 0x100;
+constexpr int kGroupM = 4;  // tile rows that are walked together
 
 // How a block's scales reach the accumulators.
 enum ScaleMode {
@@ -25,6 +58,9 @@ enum ScaleMode {
     kHardware  // E8M0 scales as operands of the matrix instruction
 };
 
+// Workgroups are dealt to the 8 XCDs in turn: each takes a contiguous range of an
+// order that walks kGroupM tile rows column by column, so that an L2 holds what
+// its workgroups share.
 __device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int& tm, int& tn) {
     const int n = tiles_m * tiles_n;
     int id = blockIdx.x;
@@ -51,7 +87,7 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
 // 16 bytes per lane from base + off straight to LDS: lane l's at lds + 16 l.
 // In assembly because the compiler, which cannot tell the two halves of the
 // double buffer apart, would wait for the load at the next LDS read; it has no
-// register output, and wait_staged() below waits for it.
+// register output, and wait_loads() below waits for it.
 __device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
 }
@@ -205,9 +241,8 @@ __global__ __launch_bounds__(MW * 128 * KG, 2) void gemm_fp8_kernel(GemmFp8Args 
     // the barrier that hands its buffer to the loads of chunk k + STAGES, between
     // the reads of the next chunk's first fragments, so that neither the barrier
     // nor the first reads leave the matrix cores idle (1024 x 4096 x 4096, one
-    // workgroup per CU: 32.9 -> 25.8 us).  Widened fragments
-    // leave no registers to hold them across the barrier (wgrad 4096 x 4096 x
-    // 8192: 262 against 272 us).
+    // workgroup per CU: 32.9 -> 26 us).  Widened fragments leave no registers to
+    // hold them across the barrier (4096 x 4096 x 8192: 262 us, so 272).
     constexpr bool kLate = !EXACT;
     auto value = [&](uint32_t w) __attribute__((always_inline)) { return E8M0 ? e8m0_value(w & 0xFFu) : __uint_as_float(w); };
     auto raw = [&](const uint8_t* tile, i32x4& x, i32x4& y) __attribute__((always_inline)) {

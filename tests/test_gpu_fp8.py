@@ -292,6 +292,92 @@ def test_gemm_larger_grids(cuda_device, shape, e8m0, out):
     assert torch.equal(c, again)  # the order of the sums is fixed
 
 
+# (M, N) that each tile size is chosen for: few rows; 64 x 64 alone on a CU and two
+# per CU; 128 x 128 alone and two per CU; 256 x 256 (bf16 results).
+VARIANTS = [(16, 700), (100, 500), (1100, 1000), (2048, 2040), (2430, 2050), (3300, 3500)]
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("e8m0", [False, True], ids=["f32s", "e8m0"])
+@pytest.mark.parametrize("shape", VARIANTS, ids=str)
+def test_gemm_every_tile_size(cuda_device, shape, e8m0, out):
+    """K of 0 to 7 blocks (groups of waves without a block, buffers that are never filled), tiles of either
+    operand, both formats: small integers under power-of-two scales, whose every sum is exact."""
+    import torch
+
+    M, N = shape
+    rng = np.random.default_rng(M + N)
+    for K in (0, 1, 128, 130, 300, 513, 896):
+        ta, tb = bool(rng.integers(2)), bool(rng.integers(2))
+        fa, fb = int(rng.integers(2)), int(rng.integers(2))
+        nb = -(-K // 128)
+
+        def op(rows, t, fmt):
+            e = rng.integers(-2, 3, (nb, -(-rows // 128) if t else rows))
+            s = (e + 127).astype(np.uint8) if e8m0 else np.exp2(e).astype(np.float32)
+            codes = small_codes(rows, K, rng)
+            if fmt == lib.E5M2:
+                codes = np.array([0x00, 0x3C, 0x40, 0xBC, 0xC0], np.uint8)[np.searchsorted([0x00, 0x38, 0x40, 0xB8, 0xC0], codes)]
+            return to_device(codes, s, K, fmt, t), fp8.operand(codes, s, fmt, t)
+
+        (qa, a), (qb, b) = op(M, ta, fa), op(N, tb, fb)
+        c = torch.full((M, N), float("nan"), dtype=torch.float32 if out == "f32" else torch.bfloat16, device="cuda")
+        lib.gemm_fp8_nt(qa, qb, c)
+        want = (a.astype(np.float32) @ b.astype(np.float32).T)  # exact: integers below 2^24 times powers of two
+        if out == "bf16":
+            want = formats.bf16_to_f32(formats.f32_to_bf16_rne(want)).reshape(M, N)
+        assert np.array_equal(host(c.float()), want), (K, ta, tb, fa, fb)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M", [5, 200])
+def test_gemm_nan_and_infinite_codes(cuda_device, M, out):
+    """Codes that no quantizer here writes: a NaN poisons its row or column, an E5M2 infinity gives infinities."""
+    import torch
+
+    rng = np.random.default_rng(M)
+    A, B = small_codes(M, 256, rng), np.full((60, 256), 0x38, np.uint8)
+    s = lambda n: np.ones((2, n), np.float32)  # noqa: E731
+    c = torch.empty((M, 60), dtype=torch.float32 if out == "f32" else torch.bfloat16, device="cuda")
+    A[2, 130] = 0x7F
+    lib.gemm_fp8_nt(to_device(A, s(M), 256, lib.E4M3, False), to_device(B, s(60), 256, lib.E4M3, False), c)
+    nan = np.isnan(host(c.float()))
+    assert nan[2].all() and nan.sum() == 60
+    A[:] = 0
+    A[1, 5], A[3, 200], A[4, 7] = 0x7C, 0xFC, 0x7E
+    lib.gemm_fp8_nt(to_device(A, s(M), 256, lib.E5M2, False), to_device(B, s(60), 256, lib.E4M3, False), c)
+    got = host(c.float())
+    assert np.isposinf(got[1]).all() and np.isneginf(got[3]).all() and np.isnan(got[4]).all()
+    got[[1, 3, 4]] = 0
+    assert not got.any()
+
+
+def test_gemm_long_contraction(cuda_device):
+    """K past 2^20: code offsets past 2^26 within a tile; +-1 throughout, so that every sum is exact."""
+    import torch
+
+    K = (1 << 20) + 77
+    g = torch.Generator(device="cuda").manual_seed(3)
+    Kp = -(-K // 128) * 128
+
+    def op(rows, tile):
+        v = torch.randint(0, 2, (rows, Kp), generator=g, device="cuda") * 2 - 1
+        v[:, K:] = 0
+        codes = torch.where(v == 0, 0, torch.where(v > 0, 0x38, 0xB8)).to(torch.uint8)
+        scales = torch.ones((Kp // 128, -(-rows // 128) if tile else rows), device="cuda")
+        return lib.Fp8Quantized(codes, scales, K, lib.E4M3, tile), v.double()
+
+    for M, N in ((3, 40), (130, 70)):
+        (qa, a), (qb, b) = op(M, False), op(N, True)
+        ref = torch.zeros((M, N), dtype=torch.float64, device="cuda")
+        for x, y in zip(a.split(1 << 16, dim=1), b.split(1 << 16, dim=1)):
+            ref += torch.mm(x, y.t().contiguous())
+        for dt in (torch.float32, torch.bfloat16):
+            c = torch.empty((M, N), dtype=dt, device="cuda")
+            lib.gemm_fp8_nt(qa, qb, c)
+            assert torch.equal(c, ref.to(dt))
+
+
 def test_training_gemms_of_a_linear(cuda_device):
     """fprop, dgrad and wgrad of one linear with ragged sizes, from the quantizer's own operands, against
     the formulas in fp64 on the oracle's operands; and the gradients against differences of the forward

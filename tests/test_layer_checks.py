@@ -38,7 +38,7 @@ def test_exports_and_c99_header(L, tmp_path):
                         "-c", str(src), "-o", str(tmp_path / "a.o")], check=True)
 
 
-def qz(L, x=P, rows=32, cols=32, ld=32, fmt=0, st=0, tile=0, rc=P, rs=P, cc=P, cs=P):
+def qz(L, x=P, rows=32, cols=32, ld=32, fmt=0, st=0, tile=0, rc=P, rs=P, cc=2 * P, cs=2 * P):
     return L.ue5m3fp4_quantize_fp8(x, rows, cols, ld, fmt, st, tile, rc, rs, cc, cs, None)
 
 
@@ -48,6 +48,7 @@ def test_quantize_argument_checks(L):
     assert qz(L, x=None) == EINVAL
     assert qz(L, rc=None) == EINVAL and qz(L, cs=None) == EINVAL
     assert qz(L, rc=None, rs=None, cc=None, cs=None) == EINVAL
+    assert qz(L, cc=P) == EINVAL and qz(L, cs=P) == EINVAL  # one buffer for both outputs
     assert qz(L, ld=31) == ESHAPE
     assert qz(L, x=P + 8) == EALIGN and qz(L, rc=P + 8) == EALIGN and qz(L, rs=P + 4) == EALIGN
     assert qz(L, rows=1 << 31) == ERANGE and qz(L, cols=1 << 31, ld=1 << 31) == ERANGE
