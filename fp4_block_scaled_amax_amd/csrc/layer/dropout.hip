@@ -4,7 +4,13 @@
 // layout: include/ue5m3fp4_layer.h; Philox4x32-10: formats.hpp.
 //
 // One Philox call serves 8 consecutive elements (16 bits each), which is the
-// unit a thread loads (16 bytes of bf16), draws for and stores.
+// unit a thread loads (16 bytes of bf16), draws for and stores.  A thread takes 4
+// units a workgroup apart; in small tensors, which would leave CUs idle, 1.
+//
+// Bound: HBM, with the generator's arithmetic hidden under it (vector ALU busy
+// 0.28 to 0.59).  Measured on inputs rotated past the 256 MB cache: 8192 x 4096
+// fp32 + bf16 residual -> bf16 with the amax 46 us (5.8 TB/s), backward of 8192 x
+// 16384 bf16 92 us (5.8 TB/s); a plain copy runs at 5.1 to 5.4 on the same card.
 #include "../formats.hpp"
 #include "layer.hpp"
 
@@ -13,7 +19,7 @@ namespace ue5m3fp4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 4;       // units of 8 elements per thread
+constexpr int64_t kSmall = 256 * 2048;  // units that still fit one per thread of 256 CUs
 constexpr uint32_t kStream = 2; // third counter word: dropout's own stream
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -99,7 +105,7 @@ __device__ __forceinline__ void amax_commit32(uint32_t m, float* amax) {
 // VEC: units of 8 elements are 16-byte aligned in every tensor and lie in one
 // row (contiguous tensors are passed as a single row; the last, partial unit
 // of one goes element by element).  W32: every call number fits 32 bits.
-template <bool XF32, bool OF32, bool RES, bool VEC, bool W32>
+template <bool XF32, bool OF32, bool RES, bool VEC, bool W32, int kUnits>
 __global__ __launch_bounds__(kThreads) void dropout_kernel(DropoutArgs a) {
     const int64_t n = a.rows * a.cols, units = (n + 7) / 8;
     const int64_t u0 = (int64_t)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
@@ -155,11 +161,13 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(DropoutArgs a) {
 template <bool XF32, bool OF32, bool RES, bool VEC>
 void launch_w(const DropoutArgs& a, hipStream_t stream) {
     const int64_t units = (a.rows * a.cols + 7) / 8;
-    const dim3 grid((unsigned)((units + kThreads * kUnits - 1) / (kThreads * kUnits)));
-    if (units <= ((int64_t)1 << 32))
-        hipLaunchKernelGGL((dropout_kernel<XF32, OF32, RES, VEC, true>), grid, dim3(kThreads), 0, stream, a);
+    auto grid = [&](int per_thread) { return dim3((unsigned)((units + kThreads * per_thread - 1) / (kThreads * per_thread))); };
+    if (units <= kSmall)
+        hipLaunchKernelGGL((dropout_kernel<XF32, OF32, RES, VEC, true, 1>), grid(1), dim3(kThreads), 0, stream, a);
+    else if (units <= ((int64_t)1 << 32))
+        hipLaunchKernelGGL((dropout_kernel<XF32, OF32, RES, VEC, true, 4>), grid(4), dim3(kThreads), 0, stream, a);
     else
-        hipLaunchKernelGGL((dropout_kernel<XF32, OF32, RES, VEC, false>), grid, dim3(kThreads), 0, stream, a);
+        hipLaunchKernelGGL((dropout_kernel<XF32, OF32, RES, VEC, false, 4>), grid(4), dim3(kThreads), 0, stream, a);
 }
 
 template <bool XF32, bool OF32, bool RES>

@@ -32,7 +32,7 @@
 //       lane), 0.34 of the waves' to waiting at the issue
 //   8192 x 4096 x 16384, bf16, E8M0 scales    440 us  2500  MFMA busy 0.55 at
 //       1.95 GHz, vector ALU 0.20
-//   4096 x 4096 x 8192, fp32, 1-D scales      262 us  1050  bound by the vector
+//   4096 x 4096 x 8192, fp32, 1-D scales      256 us  1070  bound by the vector
 //       ALU (0.59 busy: 2 conversions, 2 multiplications and FMAs per MFMA)
 //   1 x 16384 x 4096, bf16                     12.1 us  5.5 TB/s of B
 #include "layer.hpp"
@@ -146,21 +146,21 @@ struct Frag<true, E5M2> {
     }
 };
 
-// Columns n .. n + 3 of row m of C, those that exist.
+// Columns n .. n + 3 of row m of C, those that exist.  With N no multiple of 4 the
+// rows start at any element; a 16-byte (8-byte) store may do so too.
 __device__ __forceinline__ void store4(const GemmFp8Args& g, int64_t m, int64_t n, f32x4 v) {
-    if (g.N % 4 == 0) {
-        if (n >= g.N) return;
-        if (g.c_bf16)
-            *reinterpret_cast<bf16x4*>((__bf16*)g.c + m * g.N + n) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-        else
-            *reinterpret_cast<f32x4*>((float*)g.c + m * g.N + n) = v;
+    const bf16x4 h = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+    const int64_t at = m * g.N + n;
+    if (n + 4 <= g.N) {
+        if (g.c_bf16) __builtin_memcpy((__bf16*)g.c + at, &h, sizeof h);
+        else __builtin_memcpy((float*)g.c + at, &v, sizeof v);
         return;
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 3; ++e) {
         if (n + e >= g.N) continue;
-        if (g.c_bf16) ((__bf16*)g.c)[m * g.N + n + e] = (__bf16)v[e];
-        else ((float*)g.c)[m * g.N + n + e] = v[e];
+        if (g.c_bf16) ((__bf16*)g.c)[at + e] = h[e];
+        else ((float*)g.c)[at + e] = v[e];
     }
 }
 
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(MW * 128 * KG, 2) void gemm_fp8_kernel(GemmFp8Args 
     // the reads of the next chunk's first fragments, so that neither the barrier
     // nor the first reads leave the matrix cores idle (1024 x 4096 x 4096, one
     // workgroup per CU: 32.9 -> 26 us).  Widened fragments leave no registers to
-    // hold them across the barrier (4096 x 4096 x 8192: 262 us, so 272).
+    // hold them across the barrier (4096 x 4096 x 8192: 262 us, that way 272).
     constexpr bool kLate = !EXACT;
     auto value = [&](uint32_t w) __attribute__((always_inline)) { return E8M0 ? e8m0_value(w & 0xFFu) : __uint_as_float(w); };
     auto raw = [&](const uint8_t* tile, i32x4& x, i32x4& y) __attribute__((always_inline)) {
@@ -354,6 +354,9 @@ __global__ __launch_bounds__(MW * 128 * KG, 2) void gemm_fp8_kernel(GemmFp8Args 
             read_first(base);
         }
         take_scales();
+        // the other workgroup's wave on the SIMD reads and converts meanwhile (4096 x
+        // 4096 x 8192: 265 -> 256 us; waves that share their barriers gain nothing)
+        if constexpr (EXACT && KG == 1) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
             if (j + 1 < NI) {
@@ -401,6 +404,7 @@ __global__ __launch_bounds__(MW * 128 * KG, 2) void gemm_fp8_kernel(GemmFp8Args 
             }
         } else {
             add_part(NI - 1, MI - 1);
+            if constexpr (KG == 1) __builtin_amdgcn_s_setprio(0);
         }
     }
 
