@@ -77,6 +77,16 @@ __device__ __forceinline__ float e8m0_value(uint32_t c) {
     return c == 0xFFu ? __uint_as_float(0x7FC00000u) : c == 0u ? 0x1p-127f : __uint_as_float(c << 23);
 }
 
+// Where a row keeps its eight 16-byte units: unit u at u ^ swizzle(row).  Two
+// rows fill the 64 banks; the swizzle is one-to-one over 8 row pairs, so 16 rows'
+// reads of one unit touch every bank once, and its values on row pairs 0, 1, 6, 7
+// and on 2 .. 5 are each closed under ^ 2, so that the same holds where half of
+// the rows read the unit two further, as a 16-byte read of all lanes makes them.
+__device__ __forceinline__ int swizzle(int row) {
+    const int t = row >> 1;
+    return (t & 4) | ((t & 1) << 1) | (((t >> 1) ^ (t >> 2)) & 1);
+}
+
 // The same address in every lane, as scalar registers.
 __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
     const uint64_t v = (uint64_t)p;
@@ -187,20 +197,19 @@ __global__ __launch_bounds__(MW * 128 * KG, 2) void gemm_fp8_kernel(GemmFp8Args 
     const int nchunks = (blocks - group + KG - 1) / KG;
 
     // ---- staging: one 1 KB load to LDS covers 8 rows x 128 codes; lane (r, p)
-    // = (lane / 8, lane % 8) brings 16-byte unit p ^ r of its row, so that 8 rows'
-    // reads of one unit touch each of 32 banks once (16-byte reads go 8 lanes at
-    // a time).  Offsets from the tile's first code fit 32 bits (K < 2^24).
+    // = (lane / 8, lane % 8) brings 16-byte unit p ^ swizzle(row) of its row.
+    // Offsets from the tile's first code fit 32 bits (K < 2^24).
     constexpr int LA = BM / (16 * MW), LB = BN / (16 * MW), kLoads = LA + LB + 1;
     uint32_t oa[LA], ob[LB];
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
         const int row = (wave * LA + i) * 8 + (lane >> 3);
-        oa[i] = (uint32_t)min((int64_t)row, g.M - 1 - m0) * (uint32_t)Kp + 16 * ((lane & 7) ^ (lane >> 3));
+        oa[i] = (uint32_t)min((int64_t)row, g.M - 1 - m0) * (uint32_t)Kp + 16 * ((lane & 7) ^ swizzle(row));
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
         const int row = (wave * LB + i) * 8 + (lane >> 3);
-        ob[i] = (uint32_t)min((int64_t)row, g.N - 1 - n0) * (uint32_t)Kp + 16 * ((lane & 7) ^ (lane >> 3));
+        ob[i] = (uint32_t)min((int64_t)row, g.N - 1 - n0) * (uint32_t)Kp + 16 * ((lane & 7) ^ swizzle(row));
     }
     const uint8_t* ta = g.a.codes + m0 * Kp;
     const uint8_t* tb = g.b.codes + n0 * Kp;
@@ -228,7 +237,7 @@ __global__ __launch_bounds__(MW * 128 * KG, 2) void gemm_fp8_kernel(GemmFp8Args 
     };
 
     // ---- fragment reads: units 2q and 2q + 1 of row c (tile t: row 16 t + c)
-    const int o0 = c * 128 + (((2 * q) ^ (c & 7)) << 4), o1 = o0 ^ 16;
+    const int o0 = c * 128 + (((2 * q) ^ swizzle(c)) << 4), o1 = o0 ^ 16;
     const int a_base = wm * WM * 128, b_base = BM * 128 + wn * WN * 128;
 
     f32x4 acc[NI][MI];
