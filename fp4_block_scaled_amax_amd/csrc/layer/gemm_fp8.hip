@@ -27,13 +27,13 @@
 //
 // Measured (cold operands, TFLOP/s of 2 M N K; the card's library runs 2970 in
 // 8 bits with one scale per tensor and 1540 in fp16):
-//   8192 x 16384 x 4096, bf16, fp32 scales    545 us  2020  MFMA busy 0.47 at
+//   8192 x 16384 x 4096, bf16, fp32 scales    538 us  2040  MFMA busy 0.47 at
 //       1.87 GHz; 0.38 of the cycles go to vector ALU work (4 FMAs per MFMA and
 //       lane), 0.34 of the waves' to waiting at the issue
-//   8192 x 4096 x 16384, bf16, E8M0 scales    440 us  2500  MFMA busy 0.55 at
-//       1.95 GHz, vector ALU 0.20
-//   4096 x 4096 x 8192, fp32, 1-D scales      256 us  1070  bound by the vector
-//       ALU (0.59 busy: 2 conversions, 2 multiplications and FMAs per MFMA)
+//   8192 x 4096 x 16384, bf16, E8M0 scales    432 us  2550  MFMA busy 0.58 at
+//       2.0 GHz, vector ALU 0.21
+//   4096 x 4096 x 8192, fp32, 1-D scales      250 us  1100  bound by the vector
+//       ALU (0.68 busy: per MFMA 2 conversions and 2 steps of scaling)
 //   1 x 16384 x 4096, bf16                     12.1 us  5.5 TB/s of B
 #include "layer.hpp"
 

@@ -1,7 +1,11 @@
 """The layer operators together, as a training step uses them: an 8-bit linear,
 dropout joined to the residual stream with the amax that refreshes the FP4
 tensor scale, the FP4 linear behind it, and the way back -- eagerly, on a side
-stream, captured into a graph and replayed, and from two threads at once."""
+stream, captured into a graph and replayed, and from two threads at once.
+
+(The file's name places it behind test_gpu_streams.py: the control there needs
+its side stream on another hardware queue than the default stream's, and the
+streams that are taken from torch's pool here would move it.)"""
 
 import threading
 
@@ -189,3 +193,33 @@ def test_stream_of_another_device_is_refused(cuda_device):
 
     with pytest.raises(ValueError, match="stream belongs to"):
         lib.quantize_fp8(s.b16["x"], row=s.q["xr"], stream=Elsewhere())
+
+
+def test_readme_layer_example(cuda_device):
+    """The README's second example runs as written behind the first; its GEMMs agree with fp64 products of the
+    operands they were given, its dropout with the oracle's mask."""
+    import os
+
+    import torch
+
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    ns = {}
+    for block in text.split("```python\n")[1:3]:
+        exec(compile(block[:block.index("```")], "README.md", "exec"), ns)
+    torch.cuda.synchronize()
+
+    def values(q):
+        return fp8.operand(host(q.codes), host(q.scales), q.fmt, q.tile)
+
+    rows = slice(0, 64)
+    X, W, G = ns["X8"], ns["W8"], ns["G8"]
+    for out, a, b, rel in ((ns["y"], X[0], W[0], 1e-5), (ns["dx16"], G[0], W[1], 2.0 ** -8), (ns["dw"], G[1], X[1], 1e-5)):
+        ref, _ = fp8.gemm_nt(values(a)[rows], values(b))
+        got = host(out[rows].double())
+        assert np.linalg.norm(got - ref) <= rel * np.linalg.norm(ref)
+    keep = drop_oracle.keep(tuple(ns["h"].shape), 0.1, 1234, 0)
+    want = formats.f32_to_bf16_rne(drop_oracle.dropout(host(ns["y"]), keep, 0.1))
+    assert np.array_equal(host(ns["h"].float()), formats.bf16_to_f32(want).reshape(keep.shape))
+    assert host(ns["amax"])[0] == np.abs(formats.bf16_to_f32(want)).max()
+    dz = formats.f32_to_bf16_rne(drop_oracle.dropout(host(ns["dy"].float()), keep, 0.1))
+    assert np.array_equal(host(ns["dz"].float()), formats.bf16_to_f32(dz).reshape(keep.shape))
