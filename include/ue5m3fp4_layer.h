@@ -60,7 +60,8 @@ enum ue5m3fp4_data_type { UE5M3FP4_BF16 = 0, UE5M3FP4_F32 = 1 };
  *   row_codes / row_scales: x blocked along cols;
  *   col_codes / col_scales: x^T (a cols x rows operand) blocked along rows,
  *       from the same read of x.
- * Each pair is both NULL or both non-NULL, at least one pair (EINVAL).  Any
+ * Each pair is both NULL or both non-NULL, at least one pair, and no buffer
+ * serves both orientations (EINVAL).  Any
  * rows and cols below 2^31, ld >= cols (ESHAPE), rows * ld < 2^40 (ERANGE).
  * Every byte of the outputs is written, the codes' zero padding included.
  * x and the outputs must not overlap. */

@@ -238,22 +238,28 @@ def test_gemm_nan_scale_poisons_its_row_only(cuda_device, shape, e8m0, out):
     assert nan[:, N - 1].all() and nan.sum() == M
 
 
-def test_gemm_extreme_scales(cuda_device):
-    """Scales whose product leaves fp32's normal range only in the zero blocks; codes at the formats' ends."""
+@pytest.mark.parametrize("shape", [(9, 90), (70, 90), (3300, 3500)], ids=str)
+@pytest.mark.parametrize("e8m0", [False, True], ids=["f32s", "e8m0"])
+def test_gemm_extreme_scales(cuda_device, shape, e8m0):
+    """Scales whose product leaves fp32's normal range only in the zero blocks."""
     import torch
 
+    M, N = shape
     rng = np.random.default_rng(5)
-    A, B = small_codes(70, 384, rng), small_codes(90, 384, rng)
-    sa = np.full((3, 70), 2.0 ** 100, np.float32)
-    sb = np.full((3, 90), 2.0 ** -110, np.float32)
-    sa[1], sb[1] = 2.0 ** -126, 2.0 ** -126  # a block of zeros on either side
+    A, B = small_codes(M, 384, rng), small_codes(N, 384, rng)
     A[:, 128:256] = 0
-    for dt in (torch.float32, torch.bfloat16):
-        c = torch.empty((70, 90), dtype=dt, device="cuda")
-        lib.gemm_fp8_nt(to_device(A, sa, 384, lib.E4M3, False), to_device(B, sb, 384, lib.E4M3, False), c)
-        ref = (fp8.operand(A, sa, lib.E4M3, False) @ fp8.operand(B, sb, lib.E4M3, False).T).astype(np.float32)
-        want = ref if dt == torch.float32 else formats.bf16_to_f32(formats.f32_to_bf16_rne(ref))
-        assert np.array_equal(host(c.float()), want)
+    for ea, eb in ((100, -110), (-127, 120), (119, -127)):
+        sa, sb = np.full((3, M), ea), np.full((3, N), eb)
+        sa[1], sb[1] = -126, -126  # a block of zeros on one side, the least scales on both
+        scales = [(e + 127).astype(np.uint8) if e8m0 else np.ldexp(np.float32(1), e).astype(np.float32) for e in (sa, sb)]
+        qa, qb = to_device(A, scales[0], 384, lib.E4M3, False), to_device(B, scales[1], 384, lib.E4M3, False)
+        a, b = fp8.operand(A, scales[0], lib.E4M3, False), fp8.operand(B, scales[1], lib.E4M3, False)
+        ref = np.ldexp(((np.ldexp(a, -ea)).astype(np.float32) @ (np.ldexp(b, -eb)).astype(np.float32).T), ea + eb)
+        for dt in (torch.float32, torch.bfloat16):
+            c = torch.empty((M, N), dtype=dt, device="cuda")
+            lib.gemm_fp8_nt(qa, qb, c)
+            want = ref if dt == torch.float32 else formats.bf16_to_f32(formats.f32_to_bf16_rne(ref)).reshape(M, N)
+            assert np.array_equal(host(c.float()), want), (ea, eb, dt)
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
