@@ -445,14 +445,14 @@ __global__ __launch_bounds__(MW * 128 * KG, 2) void gemm_fp8_kernel(GemmFp8Args 
     }
 }
 
-// At most 16 rows of A: the time is that of reading B once.  A workgroup owns 16
-// rows of B and all of A; its waves take every W-th block of K straight from
-// memory (no wave shares another's codes, so LDS would only add a trip), four
-// blocks in flight, and their sums meet in LDS in a fixed order.
-template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int W>
+// Few rows of A (MT tiles of 16): the time is that of reading B once.  A workgroup
+// owns 16 rows of B and all of A; its waves take every W-th block of K straight
+// from memory (no wave shares another's codes, so LDS would only add a trip),
+// several blocks in flight, and their sums meet in LDS in a fixed order.
+template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int W, int MT>
 __global__ __launch_bounds__(W * 64) void gemm_fp8_skinny_kernel(GemmFp8Args g) {
-    constexpr int kDepth = 4;
-    __shared__ __align__(16) f32x4 sums[W][64];
+    constexpr int kDepth = MT == 1 ? 4 : 2;
+    __shared__ __align__(16) f32x4 sums[MT][W][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
@@ -461,10 +461,15 @@ __global__ __launch_bounds__(W * 64) void gemm_fp8_skinny_kernel(GemmFp8Args g) 
     const int nchunks = (int)(Kp / 128);
     const int64_t as_step = g.a.tile ? (g.M + 127) / 128 : g.M, bs_step = g.b.tile ? (g.N + 127) / 128 : g.N;
 
-    const int64_t m = min((int64_t)c, g.M - 1);
-    const uint8_t* pa = g.a.codes + m * Kp + 32 * q;
     const uint8_t* pb = g.b.codes + min(n0 + c, g.N - 1) * Kp + 32 * q;
-    const int64_t as_at = g.a.tile ? 0 : m;
+    const uint8_t* pa[MT];
+    int64_t as_at[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int64_t m = min((int64_t)(16 * i + c), g.M - 1);
+        pa[i] = g.a.codes + m * Kp + 32 * q;
+        as_at[i] = g.a.tile ? m >> 7 : m;
+    }
     // this lane's rows of B: as an operand row (hardware scales), or as the
     // four output columns 4 q .. 4 q + 3
     constexpr int kSb = SC == kVectorB ? 4 : 1;
@@ -479,23 +484,28 @@ __global__ __launch_bounds__(W * 64) void gemm_fp8_skinny_kernel(GemmFp8Args g) 
         else return ((const float*)base)[at];
     };
 
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4 acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     for (int k0 = wave; k0 < nchunks; k0 += W * kDepth) {
-        i32x4 bx[kDepth], by[kDepth], ax[kDepth], ay[kDepth];
-        float sa[kDepth], sb[kDepth][kSb];
-        int ha[kDepth], hb[kDepth];
+        i32x4 bx[kDepth], by[kDepth], ax[kDepth][MT], ay[kDepth][MT];
+        float sa[kDepth][MT], sb[kDepth][kSb];
+        int ha[kDepth][MT], hb[kDepth];
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {
             const int64_t k = min(k0 + d * W, nchunks - 1);  // past the end: read again, not used
             bx[d] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pb + k * 128));
             by[d] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pb + k * 128 + 16));
-            ax[d] = *reinterpret_cast<const i32x4*>(pa + k * 128);
-            ay[d] = *reinterpret_cast<const i32x4*>(pa + k * 128 + 16);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                ax[d][i] = *reinterpret_cast<const i32x4*>(pa[i] + k * 128);
+                ay[d][i] = *reinterpret_cast<const i32x4*>(pa[i] + k * 128 + 16);
+                if constexpr (SC == kHardware) ha[d][i] = ((const uint8_t*)g.a.scales)[k * as_step + as_at[i]];
+                else sa[d][i] = scale_at(g.a.scales, k * as_step + as_at[i]);
+            }
             if constexpr (SC == kHardware) {
-                ha[d] = ((const uint8_t*)g.a.scales)[k * as_step + as_at];
                 hb[d] = ((const uint8_t*)g.b.scales)[k * bs_step + bs_at[0]];
             } else {
-                sa[d] = scale_at(g.a.scales, k * as_step + as_at);
 #pragma unroll
                 for (int e = 0; e < kSb; ++e) sb[d][e] = scale_at(g.b.scales, k * bs_step + bs_at[e]);
             }
@@ -503,32 +513,37 @@ __global__ __launch_bounds__(W * 64) void gemm_fp8_skinny_kernel(GemmFp8Args g) 
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {
             const bool used = k0 + d * W < nchunks;  // selected, not branched on: the loads stay ahead
-            Frag<EXACT, AE5> a;
             Frag<EXACT, BE5> b;
-            a.set(ax[d], ay[d]);
             b.set(bx[d], by[d]);
-            f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-            if constexpr (SC == kHardware) {
-                z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, acc, BE5, AE5, 0, hb[d], 0, ha[d]);
-            } else if constexpr (EXACT) {
 #pragma unroll
-                for (int s = 0; s < 4; ++s) z = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.v[s], a.v[s], z, 0, 0, 0);
-            } else {
-                z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, z, BE5, AE5, 0, 0, 0, 0);
-            }
+            for (int i = 0; i < MT; ++i) {
+                Frag<EXACT, AE5> a;
+                a.set(ax[d][i], ay[d][i]);
+                f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+                if constexpr (SC == kHardware) {
+                    z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, acc[i], BE5, AE5, 0, hb[d], 0, ha[d][i]);
+                } else if constexpr (EXACT) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (SC != kHardware) z[e] = __builtin_fmaf(z[e], sa[d] * sb[d][kSb == 4 ? e : 0], acc[e]);
-                acc[e] = used ? z[e] : acc[e];
+                    for (int s = 0; s < 4; ++s) z = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.v[s], a.v[s], z, 0, 0, 0);
+                } else {
+                    z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, z, BE5, AE5, 0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (SC != kHardware) z[e] = __builtin_fmaf(z[e], sa[d][i] * sb[d][kSb == 4 ? e : 0], acc[i][e]);
+                    acc[i][e] = used ? z[e] : acc[i][e];
+                }
             }
         }
     }
-    sums[wave][lane] = acc;
-    __syncthreads();
-    if (wave > 0) return;
 #pragma unroll
-    for (int w = 1; w < W; ++w) acc += sums[w][lane];
-    if (c < g.M) store4(g, c, n0 + 4 * q, acc);
+    for (int i = 0; i < MT; ++i) sums[i][wave][lane] = acc[i];
+    __syncthreads();
+    if (wave >= MT) return;  // wave i sums and stores tile i
+    f32x4 v = sums[wave][0][lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += sums[wave][w][lane];
+    if (16 * wave + c < g.M) store4(g, 16 * wave + c, n0 + 4 * q, v);
 }
 
 template <int MW, int MI, int NI>
@@ -543,10 +558,10 @@ void launch_tiled(const GemmFp8Args& g, hipStream_t stream) {
                        dim3(MW * 128 * KG), 0, stream, g);
 }
 
-template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0>
+template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MT>
 void launch_skinny(const GemmFp8Args& g, hipStream_t stream) {
     constexpr int W = 8;
-    hipLaunchKernelGGL((gemm_fp8_skinny_kernel<EXACT, AE5, BE5, SC, E8M0, W>), dim3((unsigned)((g.N + 15) / 16)),
+    hipLaunchKernelGGL((gemm_fp8_skinny_kernel<EXACT, AE5, BE5, SC, E8M0, W, MT>), dim3((unsigned)((g.N + 15) / 16)),
                        dim3(W * 64), 0, stream, g);
 }
 
@@ -562,13 +577,15 @@ void launch_skinny(const GemmFp8Args& g, hipStream_t stream) {
 // 64 x 64 32; 4096 x 4096 x 4096: 65, in 128 x 128 78.  K in groups: 1024 x 1024
 // x 8192 (fp32) 25 us in 4 groups, 29 in 2, 36 in 1; 2048 x 2048 x 8192 72 in 2,
 // 79 in 1; a bf16 row by 16384 x 4096 is bound by memory and best at 2 groups of
-// 3 stages: 12.1, against 14.1 in 4 groups of 2.  At most 16 rows of A go to the
-// few-row kernel where small tiles would leave CUs idle (1 x 4096 x 16384: 20 us
-// against 41).
+// 3 stages: 12.1, against 14.1 in 4 groups of 2.  Few rows of A go to the few-row
+// kernel where small tiles would leave CUs idle: at most 16 with up to 255 tiles
+// (1 x 4096 x 16384: 20 us against 41), at most 32 with up to 64 (21 x 3920 x
+// 11523: 20 us against 25; at 128 tiles, 32 x 8192 x 4096, it is 15 against 11).
 template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0>
 void launch_size(const GemmFp8Args& g, hipStream_t stream) {
     const int64_t small = tiles_of<2, 2, 2>(g), medium = tiles_of<2, 4, 4>(g), large = tiles_of<4, 4, 8>(g);
-    if (g.M <= 16 && small < 256) return launch_skinny<EXACT, AE5, BE5, SC, E8M0>(g, stream);
+    if (g.M <= 16 && small < 256) return launch_skinny<EXACT, AE5, BE5, SC, E8M0, 1>(g, stream);
+    if (g.M <= 32 && small <= 64) return launch_skinny<EXACT, AE5, BE5, SC, E8M0, 2>(g, stream);
     const int64_t t_small = small <= 256 ? (EXACT ? 13 : 12) : (small + 511) / 512 * (EXACT ? 23 : 17);
     const int64_t t_medium = medium <= 256 ? (EXACT ? 36 : 26) : (medium + 511) / 512 * (EXACT ? 65 : 35);
     if constexpr (!EXACT)

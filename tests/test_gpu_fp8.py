@@ -298,9 +298,9 @@ def test_gemm_larger_grids(cuda_device, shape, e8m0, out):
     assert torch.equal(c, again)  # the order of the sums is fixed
 
 
-# (M, N) that each tile size is chosen for: few rows; 64 x 64 alone on a CU and two
+# (M, N) that each tile size is chosen for: few rows (one and two tiles); 64 x 64 alone on a CU and two
 # per CU; 128 x 128 alone and two per CU; 256 x 256 (bf16 results).
-VARIANTS = [(16, 700), (100, 500), (1100, 1000), (2048, 2040), (2430, 2050), (3300, 3500)]
+VARIANTS = [(16, 700), (29, 700), (100, 500), (1100, 1000), (2048, 2040), (2430, 2050), (3300, 3500)]
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
