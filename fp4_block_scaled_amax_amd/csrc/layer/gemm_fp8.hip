@@ -25,8 +25,8 @@
 // is multiplied; each wave multiplies MI x NI tiles.  launch_size() picks the
 // workgroup's tile.
 //
-// Measured (cold operands, TFLOP/s of 2 M N K; the card's library runs 2970 in
-// 8 bits with one scale per tensor and 1540 in fp16):
+// Measured (cold operands, TFLOP/s of 2 M N K, +-3 % from card to card; the card's
+// library runs 2980 in 8 bits with one scale per tensor and 1580 in fp16):
 //   8192 x 16384 x 4096, bf16, fp32 scales    538 us  2040  MFMA busy 0.47 at
 //       1.87 GHz; 0.38 of the cycles go to vector ALU work (4 FMAs per MFMA and
 //       lane), 0.34 of the waves' to waiting at the issue
