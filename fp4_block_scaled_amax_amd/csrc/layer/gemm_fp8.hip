@@ -87,10 +87,14 @@ __device__ __forceinline__ int swizzle(int row) {
     return (t & 4) | ((t & 1) << 1) | (((t >> 1) ^ (t >> 2)) & 1);
 }
 
-// The same address in every lane, as scalar registers.
+// The same address in every lane, as scalar registers.  The s_nop is the wait of 5
+// states that a vector memory instruction needs before it reads a scalar register
+// that a vector instruction wrote; the compiler inserts it for its own
+// instructions, but does not look into the assembly below.
 __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
     const uint64_t v = (uint64_t)p;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+    uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+    asm volatile("s_nop 4" : "+s"(lo), "+s"(hi));
     return (const uint8_t*)(((uint64_t)hi << 32) | lo);
 }
 
