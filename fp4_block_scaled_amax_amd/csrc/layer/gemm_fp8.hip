@@ -27,10 +27,9 @@
 //
 // Measured (cold operands, TFLOP/s of 2 M N K, +-3 % from card to card; the card's
 // library runs 2980 in 8 bits with one scale per tensor and 1580 in fp16):
-//   8192 x 16384 x 4096, bf16, fp32 scales    538 us  2040  MFMA busy 0.47 at
-//       1.87 GHz; 0.38 of the cycles go to vector ALU work (4 FMAs per MFMA and
-//       lane), 0.34 of the waves' to waiting at the issue
-//   8192 x 4096 x 16384, bf16, E8M0 scales    432 us  2550  MFMA busy 0.58 at
+//   8192 x 16384 x 4096, bf16, fp32 scales    524 us  2100  MFMA busy about 0.48
+//       at 1.9 GHz, the vector ALU 0.38 (4 FMAs per MFMA and lane)
+//   8192 x 4096 x 16384, bf16, E8M0 scales    426 us  2580  MFMA busy 0.58 at
 //       2.0 GHz, vector ALU 0.21
 //   4096 x 4096 x 8192, fp32, 1-D scales      250 us  1100  bound by the vector
 //       ALU (0.68 busy: per MFMA 2 conversions and 2 steps of scaling)
@@ -321,6 +320,9 @@ __global__ __launch_bounds__(MW * 128 * KG, 2) void gemm_fp8_kernel(GemmFp8Args 
                 z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j & kB1].v, a[i].v, z, BE5, AE5, 0, 0, 0, 0);
                 part[j & 1][i] = z;
                 if (j > 0) add_part(j - 1, i);
+                // in this order: brought together with the instruction that made
+                // them, the sums would be waited for (fprop 544 -> 524 us)
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
     };
@@ -384,6 +386,7 @@ __global__ __launch_bounds__(MW * 128 * KG, 2) void gemm_fp8_kernel(GemmFp8Args 
             if (kLate && j + 1 == NI) break;
 #pragma unroll
             for (int i = 0; i < MI; ++i) multiply(j, i);
+            if constexpr (SC == kHardware) __builtin_amdgcn_sched_barrier(0);  // dgrad 436 -> 426 us
             if constexpr (EXACT) {
                 if (j + 1 < NI) b[0].set(x, y);
             }
