@@ -94,7 +94,7 @@ int ue5m3fp4_gemm_fp8_nt(const uint8_t* a_codes, const void* a_scales, int a_for
         return UE5M3FP4_EALIGN;
     const GemmFp8Args g{{a_codes, a_scales, a_format == UE5M3FP4_E5M2, a_tile == 1},
                         {b_codes, b_scales, b_format == UE5M3FP4_E5M2, b_tile == 1},
-                        scale_type == UE5M3FP4_SCALE_E8M0, M, N, K, c, c_type == UE5M3FP4_BF16};
+                        scale_type == UE5M3FP4_SCALE_E8M0, M, N, K, c, c_type == UE5M3FP4_BF16, 0};
     clear_stale_error();
     launch_gemm_fp8(g, (hipStream_t)stream);
     return launch_status();

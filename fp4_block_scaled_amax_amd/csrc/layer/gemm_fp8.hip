@@ -60,9 +60,8 @@ enum ScaleMode {
 // Workgroups are dealt to the 8 XCDs in turn: each takes a contiguous range of an
 // order that walks kGroupM tile rows column by column, so that an L2 holds what
 // its workgroups share.
-__device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int& tm, int& tn) {
+__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
     const int n = tiles_m * tiles_n;
-    int id = blockIdx.x;
     const int per_xcd = n / 8;
     if (id < per_xcd * 8) id = (id % 8) * per_xcd + id / 8;  // the tail keeps its id
     const int width = kGroupM * tiles_n;
@@ -192,7 +191,7 @@ __global__ __launch_bounds__(MW * 128 * KG, 2) void gemm_fp8_kernel(GemmFp8Args 
     const int c = lane & 15, q = lane >> 4;
 
     int tm, tn;
-    tile_of((int)((g.M + BM - 1) / BM), (int)((g.N + BN - 1) / BN), tm, tn);
+    tile_of((int)(blockIdx.x + g.first), (int)((g.M + BM - 1) / BM), (int)((g.N + BN - 1) / BN), tm, tn);
     const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
     const int64_t Kp = (g.K + 127) / 128 * 128;
     // group g of KG takes blocks g, g + KG, ...; every group makes the same turns
@@ -561,8 +560,12 @@ int64_t tiles_of(const GemmFp8Args& g) {
 
 template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MW, int MI, int NI, int STAGES, int KG>
 void launch_tiled(const GemmFp8Args& g, hipStream_t stream) {
-    hipLaunchKernelGGL((gemm_fp8_kernel<EXACT, AE5, BE5, SC, E8M0, MW, MI, NI, STAGES, KG>), dim3((unsigned)tiles_of<MW, MI, NI>(g)),
-                       dim3(MW * 128 * KG), 0, stream, g);
+    constexpr int kThreads = MW * 128 * KG;
+    in_launches(tiles_of<MW, MI, NI>(g), kThreads, [&](int64_t first, dim3 grid) {
+        GemmFp8Args part = g;
+        part.first = first;
+        hipLaunchKernelGGL((gemm_fp8_kernel<EXACT, AE5, BE5, SC, E8M0, MW, MI, NI, STAGES, KG>), grid, dim3(kThreads), 0, stream, part);
+    });
 }
 
 template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0, int MT>

@@ -7,6 +7,19 @@
 
 namespace ue5m3fp4 {
 
+// A grid of any number of workgroups, as launches of at most 2^32 - 1 threads:
+// beyond that HIP starts their number modulo 2^32, without an error.
+// launch(first, grid) starts workgroups first .. first + grid - 1; first is a
+// multiple of 8, so that the XCDs keep their turns.
+template <typename F>
+void in_launches(int64_t groups, int threads, F launch) {
+    const int64_t most = 0xFFFFFFFFll / threads / 8 * 8;
+    for (int64_t first = 0; first < groups; first += most) {
+        const int64_t rest = groups - first;
+        launch(first, dim3((unsigned)(rest < most ? rest : most)));
+    }
+}
+
 struct QuantizeFp8Args {
     const uint16_t* x;
     int64_t rows, cols, ld;
@@ -31,6 +44,7 @@ struct GemmFp8Args {
     int64_t M, N, K;
     void* c;
     bool c_bf16;
+    int64_t first;  // the launch's first tile (set by the launcher)
 };
 
 void launch_gemm_fp8(const GemmFp8Args& g, hipStream_t stream);

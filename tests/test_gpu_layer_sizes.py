@@ -1,0 +1,43 @@
+"""The largest sizes of the layer operators on the GPU: more workgroups than one
+launch holds (HIP takes fewer than 2^32 threads per grid dimension, and starts
+their number modulo 2^32 beyond)."""
+
+import pytest
+
+import fp4_block_scaled_amax_amd as lib
+
+pytestmark = pytest.mark.gpu
+
+TALL = (1 << 29) + 70  # rows of C whose 64 x 64 tiles of 512 threads pass 2^32 threads
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(TALL, 1), (1, TALL)], ids=["tall", "wide"])
+def test_gemm_empty_sum_of_many_tiles(cuda_device, shape, out):
+    import torch
+
+    c = torch.full(shape, 3.0, dtype=torch.float32 if out == "f32" else torch.bfloat16, device="cuda")
+    lib.gemm_fp8_nt(lib.empty_quantized_fp8(shape[0], 0), lib.empty_quantized_fp8(shape[1], 0), c)
+    assert not bool(c.any())
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_gemm_many_tiles(cuda_device, out):
+    """One code per row, one column: C(i) is row i's value times its tile's scale, whichever launch holds it."""
+    import torch
+
+    codes = torch.zeros((TALL, 128), dtype=torch.uint8, device="cuda")  # 64 GiB
+    i = torch.arange(TALL, device="cuda", dtype=torch.int32)
+    codes[:, 0] = (i % 7).to(torch.uint8) + 0x38  # 1, 1.125 ... 1.75
+    tiles = -(-TALL // 128)
+    scales = (1 << (torch.arange(tiles, device="cuda") % 5)).float()[None]
+    a = lib.Fp8Quantized(codes, scales, 1, lib.E4M3, True)
+    b = lib.empty_quantized_fp8(1, 1)
+    b.codes.zero_()
+    b.codes[0, 0] = 0x40  # 2
+    b.scales.fill_(0.5)
+    c = torch.full((TALL, 1), -1.0, dtype=torch.float32 if out == "f32" else torch.bfloat16, device="cuda")
+    lib.gemm_fp8_nt(a, b, c)
+    del a, codes
+    want = (1 + (i % 7).float() / 8) * (1 << (i // 128 % 5)).float()
+    assert torch.equal(c[:, 0].float(), want)
