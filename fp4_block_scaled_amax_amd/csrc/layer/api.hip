@@ -45,7 +45,7 @@ int run_dropout(const void* x, int x_type, int64_t ldx, const void* residual, in
     const uint32_t t = (uint32_t)std::nearbyint(65536.0 * p);
     const float scale = t == 65536u ? 0.0f : (float)(65536.0 / (65536.0 - (double)t));
     const DropoutArgs a{x,    residual, out,  x_type == UE5M3FP4_F32, out_type == UE5M3FP4_F32, ldx, ldr, ldo,
-                        rows, cols,     t,    scale,                  seed,                     offset, amax};
+                        rows, cols,     t,    scale,                  seed,                     offset, amax, 0};
     clear_stale_error();
     launch_dropout(a, (hipStream_t)stream);
     return launch_status();

@@ -108,7 +108,7 @@ __device__ __forceinline__ void amax_commit32(uint32_t m, float* amax) {
 template <bool XF32, bool OF32, bool RES, bool VEC, bool W32, int kUnits>
 __global__ __launch_bounds__(kThreads) void dropout_kernel(DropoutArgs a) {
     const int64_t n = a.rows * a.cols, units = (n + 7) / 8;
-    const int64_t u0 = (int64_t)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
+    const int64_t u0 = (blockIdx.x + a.first) * (kThreads * kUnits) + threadIdx.x;
     uint32_t m = 0u;
     auto words = [&](int64_t u) __attribute__((always_inline)) {
         if constexpr (W32) return sr_words32((uint32_t)u, a.offset, kStream, a.seed);
@@ -158,16 +158,21 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(DropoutArgs a) {
     if (a.amax != nullptr) amax_commit32(m, a.amax);
 }
 
+template <bool XF32, bool OF32, bool RES, bool VEC, bool W32, int kUnits>
+void launch_units(const DropoutArgs& a, int64_t units, hipStream_t stream) {
+    in_launches((units + kThreads * kUnits - 1) / (kThreads * kUnits), kThreads, [&](int64_t first, dim3 grid) {
+        DropoutArgs part = a;
+        part.first = first;
+        hipLaunchKernelGGL((dropout_kernel<XF32, OF32, RES, VEC, W32, kUnits>), grid, dim3(kThreads), 0, stream, part);
+    });
+}
+
 template <bool XF32, bool OF32, bool RES, bool VEC>
 void launch_w(const DropoutArgs& a, hipStream_t stream) {
     const int64_t units = (a.rows * a.cols + 7) / 8;
-    auto grid = [&](int per_thread) { return dim3((unsigned)((units + kThreads * per_thread - 1) / (kThreads * per_thread))); };
-    if (units <= kSmall)
-        hipLaunchKernelGGL((dropout_kernel<XF32, OF32, RES, VEC, true, 1>), grid(1), dim3(kThreads), 0, stream, a);
-    else if (units <= ((int64_t)1 << 32))
-        hipLaunchKernelGGL((dropout_kernel<XF32, OF32, RES, VEC, true, 4>), grid(4), dim3(kThreads), 0, stream, a);
-    else
-        hipLaunchKernelGGL((dropout_kernel<XF32, OF32, RES, VEC, false, 4>), grid(4), dim3(kThreads), 0, stream, a);
+    if (units <= kSmall) launch_units<XF32, OF32, RES, VEC, true, 1>(a, units, stream);
+    else if (units <= ((int64_t)1 << 32)) launch_units<XF32, OF32, RES, VEC, true, 4>(a, units, stream);
+    else launch_units<XF32, OF32, RES, VEC, false, 4>(a, units, stream);
 }
 
 template <bool XF32, bool OF32, bool RES>

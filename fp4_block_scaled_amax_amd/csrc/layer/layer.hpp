@@ -59,7 +59,8 @@ struct DropoutArgs {
     float scale;
     uint64_t seed;
     uint32_t offset;
-    float* amax;  // nullable
+    float* amax;    // nullable
+    int64_t first;  // the launch's first workgroup (set by the launcher)
 };
 
 void launch_dropout(const DropoutArgs& a, hipStream_t stream);

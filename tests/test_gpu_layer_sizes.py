@@ -2,9 +2,13 @@
 launch holds (HIP takes fewer than 2^32 threads per grid dimension, and starts
 their number modulo 2^32 beyond)."""
 
+import numpy as np
 import pytest
 
 import fp4_block_scaled_amax_amd as lib
+from oracle import dropout as oracle
+
+from devhelpers import host
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +45,24 @@ def test_gemm_many_tiles(cuda_device, out):
     del a, codes
     want = (1 + (i % 7).float() / 8) * (1 << (i // 128 % 5)).float()
     assert torch.equal(c[:, 0].float(), want)
+
+
+def test_dropout_of_many_units(cuda_device):
+    """2^37 elements and more, in place: 2^24 workgroups of 256 threads."""
+    import torch
+
+    rows, cols = (1 << 19) + 3, 1 << 18
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < rows * cols * 2 + (4 << 30):
+        pytest.skip("a bf16 tensor of 2^37 elements does not fit this GPU")
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    for part in x.split(8192):
+        part.fill_(1.0)
+    lib.dropout(x, 0.5, 0xDEADBEEF12345678, 3, x)
+    at = np.array([0, (1 << 17) - 1, 1 << 17, (1 << 19) - 1, 1 << 19, rows - 1])
+    got = host(x[torch.from_numpy(at).cuda()].float())
+    assert np.array_equal(got, np.where(oracle.keep((rows, cols), 0.5, 0xDEADBEEF12345678, 3, rows=at), np.float32(2), np.float32(0)))
+    for part in x.split(2048):
+        assert not bool((part == 1).any())
+    del x, part
+    torch.cuda.empty_cache()
