@@ -71,7 +71,7 @@ int ue5m3fp4_quantize_fp8(const uint16_t* x, int64_t rows, int64_t cols, int64_t
         !aligned16(col_scales))
         return UE5M3FP4_EALIGN;
     const QuantizeFp8Args a{x,    rows,      cols,       ld,        format == UE5M3FP4_E5M2, scale_type == UE5M3FP4_SCALE_E8M0,
-                            tile == 1, row_codes, row_scales, col_codes, col_scales};
+                            tile == 1, row_codes, row_scales, col_codes, col_scales, 0};
     clear_stale_error();
     launch_quantize_fp8(a, (hipStream_t)stream);
     return launch_status();

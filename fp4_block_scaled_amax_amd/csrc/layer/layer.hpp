@@ -28,6 +28,7 @@ struct QuantizeFp8Args {
     void* row_scales;
     uint8_t* col_codes;
     void* col_scales;
+    int64_t first;  // the launch's first tile (set by the launcher)
 };
 
 void launch_quantize_fp8(const QuantizeFp8Args& a, hipStream_t stream);

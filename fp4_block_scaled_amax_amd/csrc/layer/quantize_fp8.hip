@@ -122,7 +122,8 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_kernel(QuantizeFp8Args 
     const int t = threadIdx.x, u = t & 15, rb = t >> 4;
     const uint32_t tiles_c = (uint32_t)((a.cols + kTile - 1) / kTile);
     const uint32_t tiles_r = (uint32_t)((a.rows + kTile - 1) / kTile);
-    const uint32_t band = blockIdx.x / (kBand * tiles_c), rem = blockIdx.x - band * kBand * tiles_c;
+    const uint32_t id = blockIdx.x + (uint32_t)a.first;
+    const uint32_t band = id / (kBand * tiles_c), rem = id - band * kBand * tiles_c;
     const uint32_t height = min(kBand, tiles_r - kBand * band);
     const int64_t tr = kBand * band + rem % height, tc = rem / height;
     const int64_t R0 = tr * kTile, C0 = tc * kTile, c0 = C0 + 8 * u;
@@ -266,16 +267,20 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_kernel(QuantizeFp8Args 
     }
 }
 
+template <bool E5M2, bool E8M0, bool TILE, bool ROW, bool COL>
+void launch_tiles(const QuantizeFp8Args& a, hipStream_t stream) {
+    in_launches(((a.rows + kTile - 1) / kTile) * ((a.cols + kTile - 1) / kTile), kThreads, [&](int64_t first, dim3 grid) {
+        QuantizeFp8Args part = a;
+        part.first = first;
+        hipLaunchKernelGGL((quantize_fp8_kernel<E5M2, E8M0, TILE, ROW, COL>), grid, dim3(kThreads), 0, stream, part);
+    });
+}
+
 template <bool E5M2, bool E8M0, bool TILE>
 void launch_outputs(const QuantizeFp8Args& a, hipStream_t stream) {
-    const int64_t tiles = ((a.rows + kTile - 1) / kTile) * ((a.cols + kTile - 1) / kTile);
-    const dim3 grid((unsigned)tiles), block(kThreads);
-    if (a.row_codes && a.col_codes)
-        hipLaunchKernelGGL((quantize_fp8_kernel<E5M2, E8M0, TILE, true, true>), grid, block, 0, stream, a);
-    else if (a.row_codes)
-        hipLaunchKernelGGL((quantize_fp8_kernel<E5M2, E8M0, TILE, true, false>), grid, block, 0, stream, a);
-    else
-        hipLaunchKernelGGL((quantize_fp8_kernel<E5M2, E8M0, TILE, false, true>), grid, block, 0, stream, a);
+    if (a.row_codes && a.col_codes) launch_tiles<E5M2, E8M0, TILE, true, true>(a, stream);
+    else if (a.row_codes) launch_tiles<E5M2, E8M0, TILE, true, false>(a, stream);
+    else launch_tiles<E5M2, E8M0, TILE, false, true>(a, stream);
 }
 
 template <bool E5M2, bool E8M0>

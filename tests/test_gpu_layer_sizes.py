@@ -7,6 +7,7 @@ import pytest
 
 import fp4_block_scaled_amax_amd as lib
 from oracle import dropout as oracle
+from oracle import formats, fp8
 
 from devhelpers import host
 
@@ -66,3 +67,27 @@ def test_dropout_of_many_units(cuda_device):
         assert not bool((part == 1).any())
     del x, part
     torch.cuda.empty_cache()
+
+
+def test_transposed_quantization_of_many_tiles(cuda_device):
+    """One column of 2^31 - 1 rows: 2^24 tiles of 256 threads."""
+    import torch
+
+    R, period = (1 << 31) - 1, 128 * 5
+    v = np.random.default_rng(1).standard_normal(period, dtype=np.float32)
+    bits = formats.f32_to_bf16_rne(v).reshape(period, 1)
+    one = torch.from_numpy(bits.view(np.int16)).cuda()
+    x = one.repeat(-(-R // period), 1)[:R].contiguous().view(torch.bfloat16)
+    q = lib.empty_quantized_fp8(1, R)
+    q.codes.fill_(0x5A)
+    q.scales.fill_(-1)
+    lib.quantize_fp8(x, col=q)
+    codes, scales = fp8.quantize(bits, lib.E4M3, orientation=1)
+    whole = R // period * period
+    want = torch.from_numpy(codes).cuda().reshape(-1)
+    assert all(bool((part.view(-1, period) == want).all()) for part in q.codes[0, :whole].split(period << 15))
+    assert bool((q.scales[:whole // 128, 0].view(-1, 5) == torch.from_numpy(scales).cuda().view(-1)).all())
+    # the ragged end, its zero padding included
+    codes, scales = fp8.quantize(bits[:R - whole], lib.E4M3, orientation=1)
+    assert np.array_equal(host(q.codes[:, whole:]), codes)
+    assert np.array_equal(host(q.scales[whole // 128:]), scales)
