@@ -35,7 +35,8 @@ int run_dropout(const void* x, int x_type, int64_t ldx, const void* residual, in
     if (!(p >= 0.0 && p <= 1.0)) return UE5M3FP4_EINVAL;
     if (!residual) ldr = cols;
     if (ldr < 0) return UE5M3FP4_EINVAL;
-    if (rows >= kMaxDim || cols >= kMaxDim || too_large(rows, ldx) || too_large(rows, ldo) || too_large(rows, ldr))
+    // cols only by rows * ld: a contiguous tensor of any shape is one row
+    if (rows >= kMaxDim || cols >= kMaxElems || too_large(rows, ldx) || too_large(rows, ldo) || too_large(rows, ldr))
         return UE5M3FP4_ERANGE;
     if (rows == 0 || cols == 0) return UE5M3FP4_OK;
     if (!x || !out) return UE5M3FP4_EINVAL;

@@ -259,7 +259,8 @@ def dropout(x, p, seed, offset, out, residual=None, amax=None, stream=None):
     with probability p (to the nearest multiple of 2^-16) or scaled by 1 / (1
     - p), by the counter-based stream (seed, offset); residual, of out's type,
     or None.  amax (device fp32 scalar or None) receives max(amax, max|out|).
-    Tensors of one shape, contiguous or matrices with unit column stride."""
+    Tensors of one shape: contiguous, of any dimension and below 2^40 elements,
+    or matrices (below 2^31 rows) with unit column stride."""
     return _dropout("ue5m3fp4_dropout", x, p, seed, offset, out, residual, amax, stream, "x", "out")
 
 

@@ -103,7 +103,8 @@ UE5M3FP4_API int ue5m3fp4_gemm_fp8_nt(const uint8_t* a_codes, const void* a_scal
  *   amax_inout: nullable device fp32; receives max(*amax_inout, max|out|) over
  *       the stored values (a NaN propagates).
  * out may be x or residual itself where the types and strides agree; other
- * overlaps are not allowed.  rows, cols < 2^31, rows * ld < 2^40 (ERANGE). */
+ * overlaps are not allowed.  rows < 2^31, rows * ld < 2^40 (ERANGE); cols has
+ * no limit of its own: a contiguous tensor of any shape is also one row. */
 UE5M3FP4_API int ue5m3fp4_dropout(const void* x, int x_type, int64_t ldx, const void* residual, int64_t ldr,
                                   void* out, int out_type, int64_t ldo, int64_t rows, int64_t cols, double p,
                                   uint64_t seed, uint32_t offset, float* amax_inout, void* stream);

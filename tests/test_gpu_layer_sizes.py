@@ -1,6 +1,7 @@
 """The largest sizes of the layer operators on the GPU: more workgroups than one
 launch holds (HIP takes fewer than 2^32 threads per grid dimension, and starts
-their number modulo 2^32 beyond)."""
+their number modulo 2^32 beyond), and contiguous tensors of any dimension past
+2^31 elements."""
 
 import numpy as np
 import pytest
@@ -91,3 +92,20 @@ def test_transposed_quantization_of_many_tiles(cuda_device):
     codes, scales = fp8.quantize(bits[:R - whole], lib.E4M3, orientation=1)
     assert np.array_equal(host(q.codes[:, whole:]), codes)
     assert np.array_equal(host(q.scales[whole // 128:]), scales)
+
+
+@pytest.mark.parametrize("shape", [(2, 8192, 131080), ((1 << 31) + 24,)], ids=["3d", "1d"])
+def test_dropout_of_contiguous_tensors_past_2_31_elements(cuda_device, shape):
+    """The mask of element e is that of the tensor's matrix view."""
+    import torch
+
+    cols = 131080 if len(shape) == 3 else 8
+    x = torch.ones(shape, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty_like(x)
+    lib.dropout(x, 0.5, 7, 9, y, residual=x)
+    lib.dropout_backward(x, 0.5, 7, 9, x)
+    y, x = y.view(-1, cols), x.view(-1, cols)
+    assert torch.equal(y, x + 1)  # 3 and 2 where kept, 1 and 0 where dropped
+    rows = np.array([0, 1, (1 << 31) // cols - 1, (1 << 31) // cols, x.shape[0] - 1])
+    keep = oracle.keep(tuple(x.shape), 0.5, 7, 9, rows=rows)
+    assert np.array_equal(host(x[torch.from_numpy(rows).cuda()].float()) != 0, keep)
