@@ -1,0 +1,141 @@
+"""The two arithmetics of the 8-bit GEMM, as the header states them: what the
+8-bit matrix instructions keep of a group of products and what that costs a
+whole result, and sums over long contractions.
+
+Figures and limits.  bf16 results: of 8 consecutive products what lies within
+2^-13 of the largest is kept, which before the rounding to bf16 costs 1e-5 of
+the result's norm on normally distributed operands (stated to one digit, so
+below 2e-5) and up to 1e-4 on heavy-tailed ones."""
+
+import numpy as np
+import pytest
+
+import fp4_block_scaled_amax_amd as lib
+from oracle import formats, fp8
+from workloads import random_bf16
+
+from devhelpers import host
+from test_gpu_fp8 import bf16, random_operand, to_device
+
+pytestmark = pytest.mark.gpu
+
+STATED = {"normal": 2e-5, "heavy": 1e-4}
+
+
+def ones(blocks, rows, e8m0):
+    return np.full((blocks, rows), 127, np.uint8) if e8m0 else np.ones((blocks, rows), np.float32)
+
+
+def product(qa, qb, M, N, dt):
+    import torch
+
+    c = torch.full((M, N), float("nan"), dtype=dt, device="cuda")
+    lib.gemm_fp8_nt(qa, qb, c)
+    return host(c.double())
+
+
+@pytest.mark.parametrize("e8m0", [False, True], ids=["f32s", "e8m0"])
+@pytest.mark.parametrize("M", [16, 320], ids=["few", "tiled"])
+def test_what_is_kept_beside_a_large_product(cuda_device, M, e8m0):
+    """A pair P, -P that cancels beside a small product q in the same group of 8: q of at least 2^-13 P comes
+    back whole from both arithmetics, at every place of the group; the fp32 one keeps any q."""
+    import torch
+
+    rng = np.random.default_rng(M)
+    code = lambda e: np.uint8((e + 7) << 3)  # noqa: E731  (2^e in E4M3, e >= -6)
+    A, q = np.zeros((M, 128), np.uint8), np.zeros(M)
+    for m in range(M):
+        at = 8 * rng.integers(16) + rng.permutation(8)[:3]
+        e = 8 - m % 15                                   # q = 2^8 ... 2^-6 beside P = 2^8
+        A[m, at[0]], A[m, at[1]], A[m, at[2]] = code(8), code(8) | 0x80, code(e)
+        q[m] = 2.0 ** e
+    B = np.full((40, 128), 0x38, np.uint8)               # 1
+    qa, qb = to_device(A, ones(1, M, e8m0), 128, lib.E4M3, False), to_device(B, ones(1, 40, e8m0), 128, lib.E4M3, False)
+    exact = product(qa, qb, M, 40, torch.float32)
+    assert np.array_equal(exact, np.repeat(q[:, None], 40, 1))
+    got = product(qa, qb, M, 40, torch.bfloat16)
+    kept = q >= 2.0 ** (8 - 13)
+    assert np.array_equal(got[kept], exact[kept])
+    assert np.all(np.abs(got - exact) <= 2.0 ** (8 - 13))
+
+
+@pytest.mark.parametrize("e8m0", [False, True], ids=["f32s", "e8m0"])
+@pytest.mark.parametrize("fmt", [lib.E4M3, lib.E5M2], ids=["e4m3", "e5m2"])
+@pytest.mark.parametrize("kind", ["normal", "heavy"])
+@pytest.mark.parametrize("M,K", [(16, 128), (200, 128), (200, 1024)], ids=str)
+def test_error_before_the_rounding_to_bf16(cuda_device, M, K, kind, fmt, e8m0):
+    """Four more blocks take from each entry of a random product what A's codes can hold of it, one product
+    per entry and block (exact in either arithmetic).  E4M3 leaves 2^-16 of an entry, E5M2 2^-12, whose rounding
+    to bf16 hides nothing: the error of the random product stands in the open."""
+    import torch
+
+    N, steps = 120, 4
+    ca, sa = fp8.quantize(random_bf16((M, K), 1, kind), fmt, e8m0)
+    cb, sb = fp8.quantize(random_bf16((N, K), 2), lib.E4M3, e8m0)
+    rest = fp8.operand(ca, sa, fmt, False) @ fp8.operand(cb, sb, lib.E4M3, False).T
+    norm = np.linalg.norm(rest)
+    for _ in range(steps):
+        e = np.ceil(np.log2(np.abs(rest).max(1))).astype(np.int64) - 8      # entries / 2^e are at most 256
+        taken = fp8.encode(-rest / np.exp2(e)[:, None], fmt)
+        rest = rest + np.exp2(e)[:, None] * fp8.decode(taken, fmt)
+        block = np.zeros((M, 128), np.uint8)
+        block[:, :N] = taken
+        unit = np.zeros((N, 128), np.uint8)
+        unit[np.arange(N), np.arange(N)] = 0x38
+        ca, cb = np.concatenate([ca, block], 1), np.concatenate([cb, unit], 1)
+        sa = np.concatenate([sa, (e + 127).astype(np.uint8)[None] if e8m0 else np.exp2(e).astype(np.float32)[None]])
+        sb = np.concatenate([sb, ones(1, N, e8m0)])
+    full = K + 128 * steps
+    qa, qb = to_device(ca, sa, full, fmt, False), to_device(cb, sb, full, lib.E4M3, False)
+    # fp32 steps: at most 132 roundings a block, each at most 2^-24 of a partial sum, whose root mean square
+    # is at most the whole result's; independent of each other, they add as squares
+    steps32 = np.sqrt(132 * full / 128) * 2.0 ** -24
+    for dt, limit in ((torch.bfloat16, STATED[kind] + 2.0 ** -8 * np.linalg.norm(rest) / norm), (torch.float32, 0.0)):
+        err = np.linalg.norm(product(qa, qb, M, N, dt) - rest) / norm
+        assert err <= limit + steps32, (dt, err)
+
+
+@pytest.mark.parametrize("M,N,K", [(16, 512, 4096), (256, 250, 16384), (2100, 2100, 1024)], ids=str)
+@pytest.mark.parametrize("e8m0", [False, True], ids=["f32s", "e8m0"])
+def test_bf16_results_are_mostly_the_nearest(cuda_device, M, N, K, e8m0):
+    """E5M2 x E4M3.  An error e flips the rounding to bf16 of a value v with probability |e| / step(v) (where v
+    lies within a step is independent of e), and the mean |e| is at most its root mean square: the share of
+    entries that are not the nearest bf16 value is bounded through the stated figure, plus five standard deviations."""
+    import torch
+
+    qa, a = random_operand(M, K, lib.E5M2, e8m0, False, 3)
+    qb, b = random_operand(N, K, lib.E4M3, e8m0, True, 4)
+    ref = torch.mm(torch.from_numpy(a).cuda(), torch.from_numpy(b).cuda().t().contiguous())
+    c = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    lib.gemm_fp8_nt(qa, qb, c)
+    step = torch.exp2(torch.floor(torch.log2(ref.abs().clamp(min=2.0 ** -126))) - 7)
+    rms = ref.square().mean().sqrt()
+    share = float((STATED["normal"] * rms / step).clamp(max=1).mean())
+    off = float((c != ref.to(torch.bfloat16)).double().mean())
+    assert off <= share + 5 * np.sqrt(share / ref.numel())
+
+
+@pytest.mark.parametrize("M,N", [(3, 40), (130, 70)], ids=str)
+def test_long_contraction_under_e8m0_scales(cuda_device, M, N):
+    """K past 2^20, +-1 throughout under scales of 1: every sum is an integer below 2^24, exact in fp32."""
+    import torch
+
+    K = (1 << 20) + 77
+    g = torch.Generator(device="cuda").manual_seed(5)
+    Kp = -(-K // 128) * 128
+
+    def op(rows):
+        v = torch.randint(0, 2, (rows, Kp), generator=g, device="cuda") * 2 - 1
+        v += 2 * (torch.rand((rows, Kp), generator=g, device="cuda") < 0.25) * (v < 0)  # 5 of 8 are +1: large sums
+        v[:, K:] = 0
+        codes = torch.where(v == 0, 0, torch.where(v > 0, 0x38, 0xB8)).to(torch.uint8)
+        return lib.Fp8Quantized(codes, torch.full((Kp // 128, rows), 127, dtype=torch.uint8, device="cuda"), K, lib.E4M3), v.double()
+
+    (qa, a), (qb, b) = op(M), op(N)
+    ref = torch.zeros((M, N), dtype=torch.float64, device="cuda")
+    for x, y in zip(a.split(1 << 16, dim=1), b.split(1 << 16, dim=1)):
+        ref += torch.mm(x, y.t().contiguous())
+    for dt in (torch.float32, torch.bfloat16):
+        c = torch.empty((M, N), dtype=dt, device="cuda")
+        lib.gemm_fp8_nt(qa, qb, c)
+        assert torch.equal(c, ref.to(dt)), dt
