@@ -83,7 +83,11 @@ UE5M3FP4_API int ue5m3fp4_quantize_fp8(const uint16_t* x, int64_t rows, int64_t 
  *       heavy-tailed ones with outlier columns; a single entry, whose products
  *       may cancel, is off by at most 2^-10 sum |a b|.
  * Any M, N below 2^31 and K below 2^24 with M*N, M*K, N*K < 2^40 (ERANGE).
- * The product of the two scales of a block pair has to be finite in fp32. */
+ * The product of the two scales of a block pair is formed in fp32, rounded to
+ * nearest, and multiplies the block's sum: where that sum is not zero it has to
+ * be finite and at least 2^-126 (below, the product loses bits, and from 2^-150
+ * down the block contributes nothing).  bf16 results of E8M0 operands apply both
+ * scales exactly.  c must not overlap the operands. */
 UE5M3FP4_API int ue5m3fp4_gemm_fp8_nt(const uint8_t* a_codes, const void* a_scales, int a_format, int a_tile,
                                       const uint8_t* b_codes, const void* b_scales, int b_format, int b_tile,
                                       int scale_type, int64_t M, int64_t N, int64_t K, void* c, int c_type,
