@@ -1,6 +1,8 @@
 """The two arithmetics of the 8-bit GEMM, as the header states them: what the
 8-bit matrix instructions keep of a group of products and what that costs a
-whole result, sums over long contractions, and the product of the block scales.
+whole result, sums over long contractions, the product of the block scales,
+and the scale NaN over zero codes that the quantizer gives a block which is
+not finite.
 
 Figures and limits.  bf16 results: of 8 consecutive products what lies within
 2^-13 of the largest is kept, which before the rounding to bf16 costs 1e-5 of
@@ -170,3 +172,52 @@ def test_product_of_the_block_scales(cuda_device, M, e8m0, tile):
                 want = formats.bf16_to_f32(formats.f32_to_bf16_rne(want)).reshape(M, N)
             got = product(qa, qb, M, N, dt)
             assert np.array_equal(got, want), (ea, eb, dt)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("tile", [False, True], ids=["1d", "tile"])
+@pytest.mark.parametrize("e8m0", [False, True], ids=["f32s", "e8m0"])
+@pytest.mark.parametrize("M,N", [(9, 90), (300, 400), (3300, 3500)], ids=str)
+def test_blocks_that_are_not_finite_poison_the_product(cuda_device, M, N, e8m0, tile, out):
+    """NaN and infinities in bf16 inputs, through the quantizer's own scale NaN over zero codes: exactly the
+    entries whose row or column holds such a block are NaN, the others are those of the oracle's operands."""
+    import torch
+
+    K = 500
+    X, W = random_bf16((M, K), 7).copy(), random_bf16((N, K), 8).copy()
+    X[3, 5], X[M - 1, K - 1], X[1, 200] = 0x7FC0, 0x7F80, 0xFF80
+    W[2, 300], W[N - 1, 129] = 0xFF81, 0x7F80
+
+    def both(bits):
+        q = [lib.empty_quantized_fp8(*s, e8m0=e8m0, tile=tile) for s in (bits.shape, bits.shape[::-1])]
+        lib.quantize_fp8(bf16(bits), row=q[0], col=q[1])
+        return q
+
+    def values(bits, o):
+        return fp8.operand(*fp8.quantize(bits, fp8.E4M3, e8m0, tile, o), fp8.E4M3, tile)
+
+    dt = torch.float32 if out == "f32" else torch.bfloat16
+    x, w = random_bf16((M, K), 7), random_bf16((N, K), 8)
+    q = {"X": both(X), "W": both(W), "x": both(x), "w": both(w)}
+    v = {"X": values(X, 0), "W": values(W, 0), "x": values(x, 0), "w": values(w, 0)}
+    # fprop with the blocks on either side and on both
+    cases = [(q["X"][0], q["w"][0], v["X"], v["w"]), (q["x"][0], q["W"][0], v["x"], v["W"]),
+             (q["X"][0], q["W"][0], v["X"], v["W"])]
+    if M < 1000:  # dgrad and wgrad
+        G = random_bf16((M, N), 9)
+        g = both(G)
+        cases += [(g[0], q["W"][1], values(G, 0), values(W, 1)), (g[1], q["X"][1], values(G, 1), values(X, 1))]
+    for qa, qb, a, b in cases:
+        rows, cols = np.isnan(a).any(1), np.isnan(b).any(1)
+        got = product(qa, qb, a.shape[0], b.shape[0], dt)
+        nan = rows[:, None] | cols[None]
+        assert 0 < nan.sum() and np.array_equal(np.isnan(got), nan)
+        a, b = a[~rows], b[~cols]
+        if not a.size or not b.size:
+            continue
+        at = np.linspace(0, a.shape[0] - 1, 40).astype(int)
+        ref, sab = a[at] @ b.T, np.abs(a[at]) @ np.abs(b).T
+        bound = (130 + -(-a.shape[1] // 128)) * 2.0 ** -24 * sab
+        if out == "bf16":
+            bound = 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * (2.0 ** -10 * sab + bound)
+        assert np.all(np.abs(got[~rows][at][:, ~cols] - ref) <= bound)
