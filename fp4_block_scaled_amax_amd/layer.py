@@ -261,8 +261,9 @@ def _dropout(where, x, p, seed, offset, out, residual, amax, stream, nx, nout):
 def dropout(x, p, seed, offset, out, residual=None, amax=None, stream=None):
     """out = residual + dropout(x): each element of x (bf16 or fp32) is zeroed
     with probability p (to the nearest multiple of 2^-16) or scaled by 1 / (1
-    - p), by the counter-based stream (seed, offset); residual, of out's type,
-    or None.  amax (device fp32 scalar or None) receives max(amax, max|out|).
+    - p), by the counter-based stream (seed, offset), which are values of the
+    call: a captured graph repeats its mask at every replay.  residual: of
+    out's type, or None.  amax (device fp32 scalar or None) receives max(amax, max|out|).
     Tensors of one shape: contiguous, of any dimension and below 2^40 elements,
     or matrices (below 2^31 rows) with unit column stride."""
     return _dropout("ue5m3fp4_dropout", x, p, seed, offset, out, residual, amax, stream, "x", "out")

@@ -107,6 +107,10 @@ UE5M3FP4_API int ue5m3fp4_gemm_fp8_nt(const uint8_t* a_codes, const void* a_scal
  *       type; row strides ldx, ldr, ldo in elements (each >= cols; ldr is
  *       not read without a residual).
  *   p in [0, 1] (EINVAL otherwise);
+ *   seed, offset: values of the call, so that a captured graph draws the same
+ *       mask at every replay.  A step that is captured and replayed needs a
+ *       graph per offset, or its dropout calls (forward and backward, which
+ *       share an offset) outside the graph;
  *   amax_inout: nullable device fp32; receives max(*amax_inout, max|out|) over
  *       the stored values (a NaN propagates).
  * out may be x or residual itself where the types and strides agree; other
