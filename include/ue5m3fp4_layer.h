@@ -112,7 +112,8 @@ UE5M3FP4_API int ue5m3fp4_gemm_fp8_nt(const uint8_t* a_codes, const void* a_scal
  *       graph per offset, or its dropout calls (forward and backward, which
  *       share an offset) outside the graph;
  *   amax_inout: nullable device fp32; receives max(*amax_inout, max|out|) over
- *       the stored values (a NaN propagates).
+ *       the stored values (a NaN propagates).  It starts at 0 or an earlier
+ *       amax: values with a sign, -0 included, are kept as they are.
  * out may be x or residual itself where the types and strides agree; other
  * overlaps are not allowed.  rows < 2^31, rows * ld < 2^40 (ERANGE); cols has
  * no limit of its own: a contiguous tensor of any shape is also one row. */
