@@ -109,3 +109,30 @@ def test_dropout_of_contiguous_tensors_past_2_31_elements(cuda_device, shape):
     rows = np.array([0, 1, (1 << 31) // cols - 1, (1 << 31) // cols, x.shape[0] - 1])
     keep = oracle.keep(tuple(x.shape), 0.5, 7, 9, rows=rows)
     assert np.array_equal(host(x[torch.from_numpy(rows).cuda()].float()) != 0, keep)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1480, 2900], ids=["128", "256"])
+def test_gemm_longest_contraction(cuda_device, n, out):
+    """K of 2^24 - 1: code offsets within a tile of 128 (256) rows pass 2^31 (come near 2^32).  +-1 in five
+    patterns a side: every sum is an integer of at most 2^24, exact in fp32."""
+    import torch
+
+    K, D = (1 << 24) - 1, 5
+    g = torch.Generator(device="cuda").manual_seed(n)
+    pats = [torch.randint(0, 2, (D, K + 1), generator=g, device="cuda", dtype=torch.int8) * 2 - 1 for _ in range(2)]
+    ref = torch.zeros((D, D), dtype=torch.float64, device="cuda")
+    ops, i = [], torch.arange(n, device="cuda") % D
+    for p in pats:
+        p[:, K:] = 0
+        codes = torch.where(p == 0, 0, torch.where(p > 0, 0x38, 0xB8)).to(torch.uint8)
+        tile = not ops  # A under tile scales, B under 1-D ones
+        scales = torch.ones(((K + 1) // 128, -(-n // 128) if tile else n), device="cuda")
+        ops.append(lib.Fp8Quantized(codes[i], scales, K, lib.E4M3, tile))
+    for x, y in zip(pats[0].split(1 << 20, dim=1), pats[1].split(1 << 20, dim=1)):
+        ref += torch.mm(x.double(), y.double().t().contiguous())
+    c = torch.full((n, n), float("nan"), dtype=torch.float32 if out == "f32" else torch.bfloat16, device="cuda")
+    lib.gemm_fp8_nt(*ops, c)
+    assert torch.equal(c, ref[i][:, i].to(c.dtype))
+    del ops
+    torch.cuda.empty_cache()
