@@ -1,5 +1,6 @@
 """CPU test of the inline assembly in the layer's kernels: a statement that
-writes m0 says so, and one that reads or writes memory is volatile and clobbers
+writes m0 has it as an output (it is a reserved register, whose clobber tells
+the compiler nothing), and one that touches memory is volatile and clobbers
 memory, since the compiler does not look inside."""
 
 import glob
@@ -30,18 +31,18 @@ def statements():
                     start = at + 1
             parts.append(body[start:])
             code = parts[0].replace("\\n", " ").replace("\\t", " ")
-            yield os.path.basename(path), m.group(1) is not None, code, parts[3] if len(parts) > 3 else ""
+            yield os.path.basename(path), m.group(1) is not None, code, parts[1] if len(parts) > 1 else "", parts[3] if len(parts) > 3 else ""
 
 
 def test_clobbers():
     loads = 0
-    for name, volatile, code, clobbers in statements():
-        if re.search(r"\bs_mov_b32 m0\b", code):
-            assert '"m0"' in clobbers, (name, code)
+    for name, volatile, code, outputs, clobbers in statements():
+        assert ("m0" in code) == ('"=&{m0}"' in outputs) and '"m0"' not in clobbers, (name, code)
         if re.search(r"\b(global|buffer|flat|ds)_(load|store|read|write|atomic)\w*", code):
             assert volatile and '"memory"' in clobbers, (name, code)
-            assert "m0" in code or "lds" not in code, (name, code)
-            loads += 1
+            if "_lds_" in code:  # the address in LDS, and the state between its write and the load
+                assert re.match(r'\s*"s_mov_b32 m0, %\d\s+s_nop 0\s+global_load_lds_', code), (name, code)
+                loads += 1
         if "s_waitcnt" in code:
             assert volatile and '"memory"' in clobbers, (name, code)
     assert loads >= 3  # the loads to LDS were found
