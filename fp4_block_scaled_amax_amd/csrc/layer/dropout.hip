@@ -10,7 +10,9 @@
 // Bound: HBM, with the generator's arithmetic hidden under it (vector ALU busy
 // 0.28 to 0.59).  Measured on inputs rotated past the 256 MB cache: 8192 x 4096
 // fp32 + bf16 residual -> bf16 with the amax 46 us (5.8 TB/s), backward of 8192 x
-// 16384 bf16 92 us (5.8 TB/s); a plain copy runs at 5.1 to 5.4 on the same card.
+// 16384 bf16 92 us (5.8 TB/s); a plain copy runs at 5.1 to 5.5 on the same card.
+// Rows that do not start at whole units (an odd row stride, or odd columns in
+// wider rows) go element by element: 8192 x 4096 bf16 92 us, against 26.
 #include "../formats.hpp"
 #include "layer.hpp"
 

@@ -29,13 +29,14 @@
 //
 // Measured (cold operands, TFLOP/s of 2 M N K, +-3 % from card to card; the card's
 // library runs 2980 in 8 bits with one scale per tensor and 1580 in fp16):
-//   8192 x 16384 x 4096, bf16, fp32 scales    524 us  2100  MFMA busy about 0.48
-//       at 1.9 GHz, the vector ALU 0.38 (4 FMAs per MFMA and lane)
-//   8192 x 4096 x 16384, bf16, E8M0 scales    426 us  2580  MFMA busy 0.58 at
-//       2.0 GHz, vector ALU 0.21
+//   8192 x 16384 x 4096, bf16, fp32 scales    524 us  2100  MFMA busy 0.49 at 1.8
+//       to 1.95 GHz, the vector ALU 0.40, waves waiting 0.37 of their time (the
+//       4 FMAs per MFMA and lane alone would cost 9 to 17 %)
+//   8192 x 4096 x 16384, bf16, E8M0 scales    426 us  2580  MFMA busy 0.57 at 1.9
+//       to 2.0 GHz, vector ALU 0.21
 //   4096 x 4096 x 8192, fp32, 1-D scales      250 us  1100  bound by the vector
-//       ALU (0.68 busy: per MFMA 2 conversions and 2 steps of scaling)
-//   1 x 16384 x 4096, bf16                     12.1 us  5.5 TB/s of B
+//       ALU (0.67 busy: per MFMA 2 conversions and 2 steps of scaling)
+//   1 x 16384 x 4096, bf16                     11.8 us  5.7 TB/s of B
 #include "layer.hpp"
 
 namespace ue5m3fp4 {
@@ -596,8 +597,8 @@ void launch_skinny(const GemmFp8Args& g, hipStream_t stream) {
 // 79 in 1; a bf16 row by 16384 x 4096 is bound by memory and best at 2 groups of
 // 3 stages: 12.1, against 14.1 in 4 groups of 2.  Few rows of A go to the few-row
 // kernel where small tiles would leave CUs idle: at most 16 with up to 255 tiles
-// (1 x 4096 x 16384: 20 us against 41), at most 32 with up to 64 (21 x 3920 x
-// 11523: 20 us against 25; at 128 tiles, 32 x 8192 x 4096, it is 15 against 11).
+// (1 x 4096 x 16384: 17 us against 37), at most 32 with up to 64 (21 x 3920 x
+// 11523: 19 us against 27; at 128 tiles, 32 x 8192 x 4096, it is 15 against 11).
 template <bool EXACT, bool AE5, bool BE5, int SC, bool E8M0>
 void launch_size(const GemmFp8Args& g, hipStream_t stream) {
     const int64_t small = tiles_of<2, 2, 2>(g), medium = tiles_of<2, 4, 4>(g), large = tiles_of<4, 4, 8>(g);
