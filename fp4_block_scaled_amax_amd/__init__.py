@@ -463,3 +463,9 @@ def update_tensor_scale(amax_running, tensor_scale, step, period=1,
 from .layer import (E4M3, E5M2, FP8_BLOCK, LAYER_LIB_PATH, Fp8Quantized, dropout,  # noqa: E402,F401
                     dropout_backward, empty_quantized_fp8, gemm_fp8_dgrad, gemm_fp8_fprop, gemm_fp8_nt,
                     gemm_fp8_wgrad, load_layer_library, quantize_fp8)
+
+# The linears of routed experts and products of bf16 tokens with FP4 weights
+# (libue5m3fp4_experts.so).
+from .experts import (EXPERTS_LIB_PATH, ExpertWeights, empty_expert_weights, gemm_grouped_dgrad,  # noqa: E402,F401
+                      gemm_grouped_fprop, gemm_grouped_wgrad, gemm_weight_only, load_experts_library,
+                      quantize_grouped, rows_padded)

@@ -1,4 +1,4 @@
-"""Build libue5m3fp4.so and libue5m3fp4_layer.so (gfx950) in-tree with hipcc.
+"""Build libue5m3fp4.so, libue5m3fp4_layer.so and libue5m3fp4_experts.so (gfx950) in-tree with hipcc.
 
 Usage: python -m fp4_block_scaled_amax_amd.build   (or build() from Python)
 """
@@ -16,6 +16,10 @@ SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemm_mx.hip"]
 # the operators next to the FP4 linears, a library of their own
 LAYER_LIB = os.path.join(PKG, "libue5m3fp4_layer.so")
 LAYER_SOURCES = ["layer/api.hip", "layer/quantize_fp8.hip", "layer/gemm_fp8.hip", "layer/dropout.hip"]
+# the linears of routed experts and the weight-only product, a third one
+EXPERTS_LIB = os.path.join(PKG, "libue5m3fp4_experts.so")
+EXPERTS_SOURCES = ["experts/api.hip", "experts/quantize_grouped.hip", "experts/gemm_grouped.hip",
+                   "experts/gemm_weight_only.hip"]
 
 HIP_FLAGS = [
     "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC",
@@ -37,6 +41,7 @@ HIP_FLAGS = [
 SOURCE_FLAGS = {
     "gemm.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
     "gemm_mx.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
+    "experts/gemm_grouped.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
 }
 
 
@@ -105,10 +110,10 @@ def build(verbose=False):
             print(out, file=sys.stderr)
         return obj
 
-    sources = SOURCES + LAYER_SOURCES
-    with ThreadPoolExecutor(max_workers=len(sources)) as ex:
+    sources = SOURCES + LAYER_SOURCES + EXPERTS_SOURCES
+    with ThreadPoolExecutor(max_workers=min(8, len(sources))) as ex:
         objs = dict(zip(sources, ex.map(compile_one, sources)))
-    for lib, members in ((LIB, SOURCES), (LAYER_LIB, LAYER_SOURCES)):
+    for lib, members in ((LIB, SOURCES), (LAYER_LIB, LAYER_SOURCES), (EXPERTS_LIB, EXPERTS_SOURCES)):
         tmp = lib + ".tmp"
         r = subprocess.run([cc, "--offload-arch=gfx950", "-shared", "-fPIC", *(objs[m] for m in members), "-o", tmp],
                            capture_output=True, text=True)
@@ -121,3 +126,4 @@ def build(verbose=False):
 if __name__ == "__main__":
     print(build(verbose=True))
     print(LAYER_LIB)
+    print(EXPERTS_LIB)

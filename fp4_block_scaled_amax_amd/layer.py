@@ -60,7 +60,12 @@ def load_layer_library(path=LAYER_LIB_PATH):
 
 
 def _launch(where, device, stream, *args):
-    """Call the entry point `where` with `args` and the stream, with `device` current."""
+    """Call the entry point `where` of this library."""
+    _enqueue(getattr(_lib or load_layer_library(), where), where, device, stream, *args)
+
+
+def _enqueue(fn, where, device, stream, *args):
+    """Call `fn`, the entry point `where`, with `args` and the stream, with `device` current."""
     import torch
 
     if stream is None:
@@ -69,7 +74,6 @@ def _launch(where, device, stream, *args):
         raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors are on {device}")
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    fn = getattr(_lib or load_layer_library(), where)
     if torch.cuda.current_device() == device.index:
         status = fn(*args, handle)
     else:
