@@ -11,6 +11,7 @@ using namespace ue5m3fp4;
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 constexpr int64_t kMaxExperts = 65536;
+constexpr int64_t kMaxTokenK = (int64_t)1 << 24;  // offsets inside a tile of the weight-only product fit 32 bits
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
@@ -113,10 +114,10 @@ int ue5m3fp4_gemm_weight_only(const uint16_t* x, int64_t ldx, const uint8_t* w_c
     if (experts < 0 || rows < 0 || N < 0 || K < 0 || ldx < 0 || ldo < 0 || !is01(out_type)) return UE5M3FP4_EINVAL;
     if (!offsets && experts > 1) return UE5M3FP4_EINVAL;
     if (w_ts_count != 1 && w_ts_count != experts) return UE5M3FP4_EINVAL;
-    if (rows >= kMaxDim || N >= kMaxDim || K >= kMaxDim || experts > kMaxExperts) return UE5M3FP4_ERANGE;
+    if (rows >= kMaxDim || N >= kMaxDim || K >= kMaxTokenK || experts > kMaxExperts) return UE5M3FP4_ERANGE;
     if (rows <= 1) ldo = N;  // a single row has no stride
     if (rows <= 1 || K == 0) ldx = (K + 7) / 8 * 8;
-    if (too_large(rows, ldx) || too_large(rows, ldo) || too_large(N, K) || too_large(experts, N * K)) return UE5M3FP4_ERANGE;
+    if (ldx >= kMaxTokenK || too_large(rows, ldx) || too_large(rows, ldo) || too_large(N, K) || too_large(experts, N * K)) return UE5M3FP4_ERANGE;
     if (K % 16 != 0) return UE5M3FP4_ESHAPE;
     if (experts == 0 || rows == 0 || N == 0) return UE5M3FP4_OK;  // nothing is read or written
     if (!w_ts || !out) return UE5M3FP4_EINVAL;
@@ -127,7 +128,7 @@ int ue5m3fp4_gemm_weight_only(const uint16_t* x, int64_t ldx, const uint8_t* w_c
         !aligned4(offsets))
         return UE5M3FP4_EALIGN;
     const WeightOnlyArgs a{x,    ldx, w_codes, w_scales, w_ts, w_ts_count == 1 ? 0 : 1, offsets, (int)experts,
-                           rows, N,   K,       out,      out_type == UE5M3FP4_OUT_BF16, ldo,     0};
+                           rows, N,   K,       out,      out_type == UE5M3FP4_OUT_BF16, ldo};
     clear_stale_error();
     launch_gemm_weight_only(a, (hipStream_t)stream);
     return launch_status();

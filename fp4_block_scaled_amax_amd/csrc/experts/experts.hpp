@@ -64,7 +64,6 @@ struct WeightOnlyArgs {
     void* out;
     bool out_bf16;
     int64_t ldo;
-    int64_t first;
 };
 
 void launch_gemm_weight_only(const WeightOnlyArgs& a, hipStream_t stream);

@@ -21,7 +21,7 @@ import os
 from dataclasses import dataclass
 
 from . import RNE, Quantized, _check_operand, _check_pair, _i64, _PKG, _require, _require_scalar
-from .layer import _address, _device_of, _enqueue, _matrix
+from .layer import _address, _enqueue, _matrix
 
 EXPERTS_LIB_PATH = os.path.join(_PKG, "libue5m3fp4_experts.so")
 
@@ -96,34 +96,98 @@ def rows_padded(rows, experts):
     return 128 * ((rows + 127) // 128 + experts)
 
 
-def _check_offsets(offsets):
+# The checks below ask each tensor once for what they need, since a call of a
+# generation step lasts little longer than its checks, and leave the messages
+# to _require and its like where something is wrong.
+
+
+def _buffer(t, dtype, dims, device, name):
+    """Shape of a contiguous `dims`-dimensional tensor of `dtype` on `device`."""
+    try:
+        shape = t.shape
+        if t.dtype is dtype and t.device == device and len(shape) == dims and t.is_contiguous():
+            return shape
+    except AttributeError:
+        pass
+    _require(t, (dtype,), name, dims, contiguous=True)
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _scalar(t, device, name):
+    """A device fp32 scalar on `device`."""
+    _require_scalar(t, name)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _rows(t, dtypes, name):
+    """(rows, cols, row stride, device) of a 2-D device tensor with unit stride along its columns."""
+    try:
+        if t.is_cuda and t.dtype in dtypes:
+            (rows, cols), (ld, unit) = t.shape, t.stride()
+            if unit == 1 or cols <= 1:
+                return rows, cols, ld if rows > 1 else cols, t.device
+    except (AttributeError, ValueError, TypeError):
+        pass
+    _require(t, dtypes, name, 2)
+    return (*_matrix(t, name), t.device)
+
+
+def _experts(offsets, device):
     """Number of experts of an offsets tensor."""
     import torch
 
-    _require(offsets, (torch.int32,), "offsets", 1, contiguous=True)
-    if offsets.numel() < 1:
+    n = _buffer(offsets, torch.int32, 1, device, "offsets")[0]
+    if n < 1:
         raise ValueError("offsets must hold experts + 1 values")
-    return offsets.numel() - 1
+    return n - 1
 
 
-def _check_weights(w, name, experts):
-    """(rows, cols) of an ExpertWeights operand with contiguous device buffers."""
+def _operand(q, device, name):
+    """(rows, cols) of a Quantized operand."""
+    import torch
+
+    if not isinstance(q, Quantized):
+        raise ValueError(f"{name} must be a Quantized operand")
+    rows, half = _buffer(q.codes, torch.uint8, 2, device, name)
+    if half % 8 != 0 or _buffer(q.scales, torch.uint8, 2, device, name) != (rows, half // 8):
+        _check_operand(q, name)
+    if q.ts.dtype is not torch.float32 or q.ts.numel() != 1 or q.ts.device != device:
+        _scalar(q.ts, device, f"{name} ts")
+    return rows, 2 * half
+
+
+def _weights(w, experts, device, name):
+    """(rows, cols) of one expert's operand in an ExpertWeights."""
     import torch
 
     if not isinstance(w, ExpertWeights):
         raise ValueError(f"{name} must be an ExpertWeights operand")
-    _require(w.codes, (torch.uint8,), name + " codes", 3, contiguous=True)
-    _require(w.scales, (torch.uint8,), name + " scales", 3, contiguous=True)
-    _require(w.ts, (torch.float32,), name + " ts", contiguous=True)
-    n, rows, half = w.codes.shape
+    n, rows, half = _buffer(w.codes, torch.uint8, 3, device, name)
     if n != experts:
         raise ValueError(f"{name} holds {n} experts, offsets {experts}")
-    if half % 8 != 0 or w.scales.shape != (n, rows, half // 8):
+    if half % 8 != 0 or _buffer(w.scales, torch.uint8, 3, device, name) != (n, rows, half // 8):
         raise ValueError(f"{name}: codes {tuple(w.codes.shape)} / scales {tuple(w.scales.shape)} do not match "
                          "([experts][R][C/2], [experts][R][C/16], C a multiple of 16)")
-    if w.ts.numel() not in (1, n):
+    if _buffer(w.ts, torch.float32, 1, device, name)[0] not in (1, n):
         raise ValueError(f"{name}: ts must hold 1 value or one per expert (has {w.ts.numel()})")
     return rows, 2 * half
+
+
+def _result(out, device, shape, name="out"):
+    """Whether a contiguous result tensor of this shape is fp32 (else bf16)."""
+    import torch
+
+    f32 = out.dtype is torch.float32
+    if _buffer(out, torch.float32 if f32 else torch.bfloat16, len(shape), device, name) != shape:
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor (has {list(out.shape)})")
+    return f32
+
+
+def _device(t, name):
+    if t is None or not getattr(t, "is_cuda", False):
+        raise ValueError(f"{name} must be a device (cuda) tensor")
+    return t.device
 
 
 def quantize_grouped(x, offsets, tensor_scale, rounding=RNE, seed=0, offset=0, row=None, col=None, index=None,
@@ -137,60 +201,49 @@ def quantize_grouped(x, offsets, tensor_scale, rounding=RNE, seed=0, offset=0, r
     padding, keep what they held."""
     import torch
 
-    _require(x, (torch.bfloat16, torch.int16, torch.uint16), "x", 2)
-    x_rows, cols, ld = _matrix(x, "x")
-    experts, rows = _check_offsets(offsets), x_rows
+    x_rows, cols, ld, device = _rows(x, (torch.bfloat16, torch.int16, torch.uint16), "x")
+    experts, rows = _experts(offsets, device), x_rows
     if index is not None:
-        _require(index, (torch.int32,), "index", 1, contiguous=True)
-        rows = index.numel()
+        rows = _buffer(index, torch.int32, 1, device, "index")[0]
     buffers = []
     for q, name, r, c in ((row, "row output", rows, cols), (col, "col output", cols, rows_padded(rows, experts))):
         if q is None:
             buffers += [None, None]
             continue
         codes, scales = (q.codes, q.scales) if isinstance(q, Quantized) else q
-        _check_pair(codes, scales, r, c, name)
+        if (_buffer(codes, torch.uint8, 2, device, name) != (r, c // 2)
+                or _buffer(scales, torch.uint8, 2, device, name) != (r, c // 16)):
+            _check_pair(codes, scales, r, c, name)
         buffers += [codes, scales]
     if row is None and col is None and amax is None:
         raise ValueError("quantize_grouped: row, col or amax is required")
     if tensor_scale is not None:
-        _require_scalar(tensor_scale, "tensor_scale")
+        _scalar(tensor_scale, device, "tensor_scale")
     elif row is not None or col is not None:
         raise ValueError("tensor_scale is required")
     if amax is not None:
-        _require_scalar(amax, "amax")
+        _scalar(amax, device, "amax")
     if not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 32:
         raise ValueError("seed must fit 64 unsigned bits and offset 32")
-    device = _device_of("quantize_grouped", x, offsets, tensor_scale, index, amax, *buffers)
     _launch("ue5m3fp4_quantize_grouped", device, stream, x.data_ptr(), x_rows, cols, ld, _address(index), rows,
             offsets.data_ptr(), experts, _address(tensor_scale), int(rounding), int(seed), int(offset),
             *map(_address, buffers), _address(amax))
 
 
-def _check_out(out, shape, name="out"):
-    import torch
-
-    _require(out, (torch.bfloat16, torch.float32), name, len(shape), contiguous=True)
-    if out.shape != shape:
-        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor (has {list(out.shape)})")
-    return int(out.dtype == torch.float32)
-
-
 def _gemm_grouped(a, w, offsets, out, amax, stream, na, nw):
-    experts = _check_offsets(offsets)
-    _check_operand(a, na)
-    N, K = _check_weights(w, nw, experts)
-    if a.cols != K:
-        raise ValueError(f"{na} and {nw} disagree on the contraction axis ({a.cols} vs {K})")
-    f32 = _check_out(out, (a.rows, N))
+    device = _device(out, "out")
+    experts = _experts(offsets, device)
+    (rows, ak), (N, K) = _operand(a, device, na), _weights(w, experts, device, nw)
+    if ak != K:
+        raise ValueError(f"{na} and {nw} disagree on the contraction axis ({ak} vs {K})")
+    f32 = _result(out, device, (rows, N))
     if amax is not None:
-        _require_scalar(amax, "amax")
+        _scalar(amax, device, "amax")
         if f32:
             raise ValueError("amax is for bf16 outputs")
-    device = _device_of("gemm_grouped", out, a.codes, a.scales, a.ts, w.codes, w.scales, w.ts, offsets, amax)
     _launch("ue5m3fp4_gemm_grouped_nt", device, stream, a.codes.data_ptr(), a.scales.data_ptr(), a.ts.data_ptr(),
             w.codes.data_ptr(), w.scales.data_ptr(), w.ts.data_ptr(), w.ts.numel(), offsets.data_ptr(), experts,
-            a.rows, N, K, out.data_ptr(), f32, _address(amax))
+            rows, N, K, out.data_ptr(), f32, _address(amax))
     return out
 
 
@@ -211,19 +264,17 @@ def gemm_grouped_wgrad(dy_col, x_col, offsets, dw, stream=None):
     """dW [experts][out][in] (bf16 or fp32) = dY^T X over each expert's rows,
     from the grouped transposed operands of dY and X; zeros for an expert
     without rows."""
-    experts = _check_offsets(offsets)
-    _check_operand(dy_col, "dy_col")
-    _check_operand(x_col, "x_col")
-    rows = dy_col.cols - 128 * experts  # up to a multiple of 128, which rows_padded does not tell apart
-    if rows < 0 or rows % 128 != 0 or x_col.cols != dy_col.cols:
+    device = _device(dw, "dw")
+    experts = _experts(offsets, device)
+    (M, padded), (N, x_padded) = _operand(dy_col, device, "dy_col"), _operand(x_col, device, "x_col")
+    rows = padded - 128 * experts  # up to a multiple of 128, which rows_padded does not tell apart
+    if rows < 0 or rows % 128 != 0 or x_padded != padded:
         raise ValueError(f"dy_col and x_col must have rows_padded(rows, {experts}) columns "
-                         f"(have {dy_col.cols} and {x_col.cols})")
-    f32 = _check_out(dw, (experts, dy_col.rows, x_col.rows), "dw")
-    device = _device_of("gemm_grouped_wgrad", dw, dy_col.codes, dy_col.scales, dy_col.ts, x_col.codes, x_col.scales,
-                        x_col.ts, offsets)
+                         f"(have {padded} and {x_padded})")
+    f32 = _result(dw, device, (experts, M, N), "dw")
     _launch("ue5m3fp4_gemm_grouped_wgrad", device, stream, dy_col.codes.data_ptr(), dy_col.scales.data_ptr(),
             dy_col.ts.data_ptr(), x_col.codes.data_ptr(), x_col.scales.data_ptr(), x_col.ts.data_ptr(),
-            offsets.data_ptr(), experts, rows, dy_col.rows, x_col.rows, dw.data_ptr(), f32)
+            offsets.data_ptr(), experts, rows, M, N, dw.data_ptr(), f32)
     return dw
 
 
@@ -234,23 +285,20 @@ def gemm_weight_only(x, w, out, offsets=None, stream=None):
     about 64 per expert)."""
     import torch
 
-    _require(x, (torch.bfloat16, torch.int16, torch.uint16), "x", 2)
-    rows, K, ldx = _matrix(x, "x")
+    rows, K, ldx, device = _rows(x, (torch.bfloat16, torch.int16, torch.uint16), "x")
     if offsets is None:
-        experts = 1
-        _check_operand(w, "w")
-        N, wk = w.rows, w.cols
+        experts, (N, wk) = 1, _operand(w, device, "w")
     else:
-        experts = _check_offsets(offsets)
-        N, wk = _check_weights(w, "w", experts)
+        experts = _experts(offsets, device)
+        N, wk = _weights(w, experts, device, "w")
     if wk != K:
         raise ValueError(f"x and w disagree on the contraction axis ({K} vs {wk})")
-    _require(out, (torch.bfloat16, torch.float32), "out", 2)
-    if out.shape != (rows, N):
+    out_rows, out_cols, ldo, out_device = _rows(out, (torch.bfloat16, torch.float32), "out")
+    if out_rows != rows or out_cols != N:
         raise ValueError(f"out must be a [{rows}][{N}] tensor (has {list(out.shape)})")
-    ldo = _matrix(out, "out")[2]
-    device = _device_of("gemm_weight_only", out, x, w.codes, w.scales, w.ts, offsets)
+    if out_device != device:
+        raise ValueError(f"out is on {out_device}, x on {device}")
     _launch("ue5m3fp4_gemm_weight_only", device, stream, x.data_ptr(), ldx, w.codes.data_ptr(), w.scales.data_ptr(),
             w.ts.data_ptr(), w.ts.numel(), _address(offsets), experts, rows, N, K, out.data_ptr(),
-            int(out.dtype == torch.float32), ldo)
+            out.dtype is torch.float32, ldo)
     return out

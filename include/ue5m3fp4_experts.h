@@ -120,8 +120,8 @@ UE5M3FP4_API int ue5m3fp4_gemm_grouped_wgrad(const uint8_t* a_codes, const uint8
  *       [experts][N][K] with the rows grouped by offsets;
  *   w_ts: w_ts_count device fp32 values, 1 or `experts` of them (EINVAL);
  *   out: [rows][N], row stride ldo elements (ldo >= N where rows > 1: ESHAPE).
- * K % 16 == 0 (ESHAPE); rows, N, K < 2^31, rows * ldx, rows * ldo and experts
- * * N * K < 2^40 (ERANGE).  out must not overlap the inputs. */
+ * K % 16 == 0 (ESHAPE); rows, N < 2^31, K, ldx < 2^24, rows * ldx, rows * ldo
+ * and experts * N * K < 2^40 (ERANGE).  out must not overlap the inputs. */
 UE5M3FP4_API int ue5m3fp4_gemm_weight_only(const uint16_t* x, int64_t ldx, const uint8_t* w_codes,
                                            const uint8_t* w_scales, const float* w_ts, int64_t w_ts_count,
                                            const int32_t* offsets, int64_t experts, int64_t rows, int64_t N, int64_t K,
