@@ -11,7 +11,7 @@ using namespace ue5m3fp4;
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 constexpr int64_t kMaxExperts = 65536;
-constexpr int64_t kMaxTokenK = (int64_t)1 << 24;  // offsets inside a tile of the weight-only product fit 32 bits
+constexpr int64_t kMaxK = (int64_t)1 << 24;  // of a product: offsets inside a tile fit 32 bits
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
@@ -69,7 +69,7 @@ int ue5m3fp4_gemm_grouped_nt(const uint8_t* a_codes, const uint8_t* a_scales, co
     if (experts < 0 || rows < 0 || N < 0 || K < 0 || !is01(c_type)) return UE5M3FP4_EINVAL;
     if (b_ts_count != 1 && b_ts_count != experts) return UE5M3FP4_EINVAL;
     if (amax_inout && c_type != UE5M3FP4_OUT_BF16) return UE5M3FP4_EINVAL;
-    if (rows >= kMaxDim || N >= kMaxDim || K >= kMaxDim || experts > kMaxExperts) return UE5M3FP4_ERANGE;
+    if (rows >= kMaxDim || N >= kMaxDim || K >= kMaxK || experts > kMaxExperts) return UE5M3FP4_ERANGE;
     if (too_large(rows, N) || too_large(rows, K) || too_large(N, K) || too_large(experts, N * K)) return UE5M3FP4_ERANGE;
     if (K % 16 != 0) return UE5M3FP4_ESHAPE;
     if (experts == 0 || rows == 0 || N == 0) return UE5M3FP4_OK;  // nothing is read or written
@@ -93,7 +93,7 @@ int ue5m3fp4_gemm_grouped_wgrad(const uint8_t* a_codes, const uint8_t* a_scales,
     if (experts < 0 || rows < 0 || M < 0 || N < 0 || !is01(c_type)) return UE5M3FP4_EINVAL;
     if (rows >= kMaxDim || M >= kMaxDim || N >= kMaxDim || experts > kMaxExperts) return UE5M3FP4_ERANGE;
     const int64_t padded = rows_padded(rows, experts);
-    if (padded >= kMaxDim || too_large(M, padded) || too_large(N, padded) || too_large(M, N) || too_large(experts, M * N))
+    if (padded >= kMaxK || too_large(M, padded) || too_large(N, padded) || too_large(M, N) || too_large(experts, M * N))
         return UE5M3FP4_ERANGE;
     if (experts == 0 || M == 0 || N == 0) return UE5M3FP4_OK;
     if (!a_ts || !b_ts || !offsets || !c) return UE5M3FP4_EINVAL;
@@ -114,10 +114,10 @@ int ue5m3fp4_gemm_weight_only(const uint16_t* x, int64_t ldx, const uint8_t* w_c
     if (experts < 0 || rows < 0 || N < 0 || K < 0 || ldx < 0 || ldo < 0 || !is01(out_type)) return UE5M3FP4_EINVAL;
     if (!offsets && experts > 1) return UE5M3FP4_EINVAL;
     if (w_ts_count != 1 && w_ts_count != experts) return UE5M3FP4_EINVAL;
-    if (rows >= kMaxDim || N >= kMaxDim || K >= kMaxTokenK || experts > kMaxExperts) return UE5M3FP4_ERANGE;
+    if (rows >= kMaxDim || N >= kMaxDim || K >= kMaxK || experts > kMaxExperts) return UE5M3FP4_ERANGE;
     if (rows <= 1) ldo = N;  // a single row has no stride
     if (rows <= 1 || K == 0) ldx = (K + 7) / 8 * 8;
-    if (ldx >= kMaxTokenK || too_large(rows, ldx) || too_large(rows, ldo) || too_large(N, K) || too_large(experts, N * K)) return UE5M3FP4_ERANGE;
+    if (ldx >= kMaxK || too_large(rows, ldx) || too_large(rows, ldo) || too_large(N, K) || too_large(experts, N * K)) return UE5M3FP4_ERANGE;
     if (K % 16 != 0) return UE5M3FP4_ESHAPE;
     if (experts == 0 || rows == 0 || N == 0) return UE5M3FP4_OK;  // nothing is read or written
     if (!w_ts || !out) return UE5M3FP4_EINVAL;

@@ -16,14 +16,15 @@
 // v_pk_mul_f16 (by m = 8 + f, or f where e = 0): a scale byte (e, f) is expanded
 // to one dword that holds both factors, the fp32 exponent above, fp16 m below.
 //
-// Tiles.  A workgroup of 4 waves computes 256 columns of up to 256 rows of one
-// expert, in steps of 128 along the contraction, double-buffered in LDS.  The
-// more rows a wave has the fewer conversions it does per matrix instruction (4
-// VALU instructions at 128 x 128 per wave, 6 at 128 x 64, 8 at 64 x 64, 12 at 32 x
-// 64), so an expert's rows go in tiles of 256 while more than 128 are left, and
-// the rest in one tile of 128, 64 or 32 rows, whose four waves stand side by side.
-// Full tiles are dealt first, the rests after them: the short ones fill what the
-// last round of long ones leaves.
+// Tiles.  A workgroup of 4 waves computes 128 columns of up to 256 (or 128) rows of
+// one expert, in steps of 128 along the contraction, double-buffered in LDS; two
+// workgroups share a CU, so that one converts while the other multiplies, and one
+// loads its first step or stores its results while the other is in its loop.  The
+// more rows a wave has the fewer conversions it does per matrix instruction (6 VALU
+// instructions at 128 x 64 per wave, 8 at 64 x 64, 12 at 32 x 64), so an expert's
+// rows go in tiles of full height while more than half of one is left, and the rest
+// in one lower tile.  Full tiles are dealt first, the rests after them: the short
+// ones fill what the last round of long ones leaves.
 #include "../formats.hpp"
 #include "experts.hpp"
 
@@ -37,21 +38,9 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kBM = 256, kBN = 256, kBK = 128;
+constexpr int kBK = 128;
 constexpr int kThreads = 256;
-constexpr int kCodeStride = kBK / 2 + 8;  // 64 bytes per row, padded to 72
-constexpr int kCodesA = 0;
-constexpr int kCodesB = kCodesA + kBM * kCodeStride;
-constexpr int kScaleBlockStride = kBM * 4 + 32;  // a block's 256 rows, padded
-constexpr int kScalesA = kCodesB + kBN * kCodeStride;
-constexpr int kScalesB = kScalesA + 8 * kScaleBlockStride;
-constexpr int kStage = kScalesB + 8 * kScaleBlockStride;
-constexpr int kLut = 2 * kStage;
-constexpr int kSmem = kLut + 256 * 4;
 constexpr int kGroupM = 4;  // tile rows that are walked together
-
-// sched_group_barrier masks
-constexpr int kSchedMfma = 0x008, kSchedValu = 0x002, kSchedDs = 0x300, kSchedVmemRead = 0x020;
 
 // UE5M3 byte -> expanded dword (0xFF: m = NaN, which poisons what it enters).
 __device__ __forceinline__ uint32_t expand_scale(uint32_t c) {
@@ -83,37 +72,12 @@ __device__ __forceinline__ uint16_t to_bf16(float f) {
     return u;
 }
 
-// A 16-byte unit (32 codes) of a row's step at k0.  Where K is no multiple of 128
-// its halves are clamped into the row; blocks past K get the scale 0 below, whose
-// factor m = 0 makes every code 0.
-template <bool ALIGNED>
-__device__ __forceinline__ u32x4 load_unit(const uint8_t* row, int64_t K, int64_t k0, int part) {
-    if (ALIGNED) return *reinterpret_cast<const u32x4*>(row + k0 / 2 + 16 * part);
-    const int64_t ka = min(k0 + 32 * part, K - 16), kb = min(k0 + 32 * part + 16, K - 16);
-    const u32x2 x = *reinterpret_cast<const u32x2*>(row + ka / 2);
-    const u32x2 y = *reinterpret_cast<const u32x2*>(row + kb / 2);
-    return u32x4{x.x, x.y, y.x, y.y};
-}
-
-// The 8 scale bytes of a row's step at block b0.
-template <bool ALIGNED>
-__device__ __forceinline__ u32x2 load_scales(const uint8_t* row, int64_t blocks, int64_t b0) {
-    if (ALIGNED) return *reinterpret_cast<const u32x2*>(row + b0);
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t v = row[min(b0 + j, blocks - 1)];
-        w[j >> 2] |= (b0 + j < blocks ? v : 0u) << (8 * (j & 3));
-    }
-    return u32x2{w[0], w[1]};
-}
-
 // What a workgroup computes: rows [0, rows) of A from `a` on times columns [0,
 // cols) of B from `b` on; strides in bytes.
 struct Tile {
     const uint8_t *a, *as, *b, *bs;
     int64_t a_stride, as_stride, b_stride, bs_stride;
-    int64_t K;       // contraction; strides and K are a multiple of 128 where ALIGNED
+    int64_t K;       // contraction
     int rows, cols;  // of this tile, at least 1
     int64_t c;       // element offset of its first result
     float sa256, sb;
@@ -134,121 +98,217 @@ __device__ __forceinline__ void amax_commit(uint32_t m, float* amax) {
     }
 }
 
-// One tile, by WM x WN waves of RI x CJ 32 x 32 results.  Lane (r, h) = (lane % 32,
-// lane / 32) owns elements [64 h + 16 b, + 16) of each row's step in block-step b
-// (0..3): one block, one scale, two matrix instructions.  A and B agree on it, so
-// the sums are those of the plain order.  While a step's matrix instructions issue,
-// the next step's operands are dequantized, the next block-step is read from LDS,
-// chunk c + 1 is stored to LDS and chunk c + 2 loaded; the chunk's one barrier
-// stands before its last block-step, whose operands are in registers.
-template <int RI, int CJ, int WM, int WN, bool ALIGNED>
-__device__ __forceinline__ void compute_tile(const Tile& t, uint8_t* smem, void* cptr, bool c_bf16, int64_t N,
-                                             float* amax) {
-    constexpr int kRows = 32 * RI * WM;
-    constexpr int kUnitsA = (kRows + 63) / 64;  // 16-byte units per thread and chunk
-    static_assert(32 * CJ * WN == kBN && WM * WN == 4, "4 waves, 256 columns");
-    const uint32_t* lut = reinterpret_cast<const uint32_t*>(smem + kLut);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = wave / WN, wn = wave % WN;
-    const int r = lane & 31, h = lane >> 5;
-    const int nchunks = (int)((t.K + kBK - 1) / kBK);
-    const int64_t blocks = t.K / 16;
+// LDS accesses of a wave's lanes to each other's data: the hardware keeps a wave's in
+// order, the compiler has to as well.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
 
-    // Staging: thread tid takes part spart of rows srow + 64 i of both operands,
-    // and the scales of row tid; rows past the tile are clamped (their results
-    // are not stored).  The 16 lanes that an 8-byte LDS store serves per cycle
-    // hold rows o, o + 1, o + 8, o + 9, which start 0, 18, 16 and 2 banks apart.
-    const int sq = (tid >> 2) & 15, spart = tid & 3;
-    const int srow = 16 * (tid >> 6) + 2 * (sq >> 2) + (sq & 1) + 8 * ((sq >> 1) & 1);
-    const uint8_t* a_rows[kUnitsA];
-    const uint8_t* b_rows[4];
-#pragma unroll
-    for (int i = 0; i < kUnitsA; ++i) a_rows[i] = t.a + min(srow + 64 * i, t.rows - 1) * t.a_stride;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b_rows[i] = t.b + min(srow + 64 * i, t.cols - 1) * t.b_stride;
-    const uint8_t* a_srow = t.as + min(tid, t.rows - 1) * t.as_stride;
-    const uint8_t* b_srow = t.bs + min(tid, t.cols - 1) * t.bs_stride;
-    const bool stage_a = kRows >= 64 || srow < kRows, scale_a = kRows >= kThreads || tid < kRows;
+__device__ __forceinline__ void put(float& to, float v, uint32_t&) { to = v; }
+__device__ __forceinline__ void put(uint16_t& to, float v, uint32_t& tmax) {
+    to = to_bf16(v);
+    tmax = max(tmax, (uint32_t)(to & 0x7FFFu));
+}
 
-    // plain vector values, no arrays: they stay in registers
-    u32x4 ra0, ra1, ra2, ra3, rb0, rb1, rb2, rb3;
-    u32x2 rsa, rsb;
-    auto gload = [&](int chunk) __attribute__((always_inline)) {
-        const int64_t k0 = (int64_t)chunk * kBK;
-        ra0 = load_unit<ALIGNED>(a_rows[0], t.K, k0, spart);
-        if constexpr (kUnitsA > 1) ra1 = load_unit<ALIGNED>(a_rows[1], t.K, k0, spart);
-        if constexpr (kUnitsA > 2) ra2 = load_unit<ALIGNED>(a_rows[2], t.K, k0, spart);
-        if constexpr (kUnitsA > 3) ra3 = load_unit<ALIGNED>(a_rows[3], t.K, k0, spart);
-        rb0 = load_unit<ALIGNED>(b_rows[0], t.K, k0, spart);
-        rb1 = load_unit<ALIGNED>(b_rows[1], t.K, k0, spart);
-        rb2 = load_unit<ALIGNED>(b_rows[2], t.K, k0, spart);
-        rb3 = load_unit<ALIGNED>(b_rows[3], t.K, k0, spart);
-        rsa = load_scales<ALIGNED>(a_srow, blocks, k0 / 16);
-        rsb = load_scales<ALIGNED>(b_srow, blocks, k0 / 16);
-    };
-    auto lstore_codes = [&](uint8_t* base) __attribute__((always_inline)) {
-        auto st = [](uint8_t* p, u32x4 v) __attribute__((always_inline)) {  // rows are 8-byte aligned
-            *reinterpret_cast<u32x2*>(p) = v.xy;
-            *reinterpret_cast<u32x2*>(p + 8) = v.zw;
-        };
-        uint8_t* pa = base + kCodesA + srow * kCodeStride + 16 * spart;
-        uint8_t* pb = base + kCodesB + srow * kCodeStride + 16 * spart;
-        if (stage_a) st(pa, ra0);
-        if constexpr (kUnitsA > 1) st(pa + 64 * kCodeStride, ra1);
-        if constexpr (kUnitsA > 2) st(pa + 128 * kCodeStride, ra2);
-        if constexpr (kUnitsA > 3) st(pa + 192 * kCodeStride, ra3);
-        st(pb, rb0);
-        st(pb + 64 * kCodeStride, rb1);
-        st(pb + 128 * kCodeStride, rb2);
-        st(pb + 192 * kCodeStride, rb3);
-    };
-    uint32_t ea[8], eb[8];
-    auto lut_fetch = [&]() __attribute__((always_inline)) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t wa = j < 4 ? rsa.x : rsa.y, wb = j < 4 ? rsb.x : rsb.y;
-            ea[j] = lut[(wa >> (8 * (j & 3))) & 0xFFu];
-            eb[j] = lut[(wb >> (8 * (j & 3))) & 0xFFu];
-        }
-    };
-    auto lstore_scales = [&](uint8_t* base) __attribute__((always_inline)) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (scale_a) *reinterpret_cast<uint32_t*>(base + kScalesA + j * kScaleBlockStride + tid * 4) = ea[j];
-            *reinterpret_cast<uint32_t*>(base + kScalesB + j * kScaleBlockStride + tid * 4) = eb[j];
-        }
-    };
-
-    const int a_code_off = kCodesA + (wm * 32 * RI + r) * kCodeStride + 32 * h;
-    const int b_code_off = kCodesB + (wn * 32 * CJ + r) * kCodeStride + 32 * h;
-    const int a_sc_off = kScalesA + 4 * h * kScaleBlockStride + (wm * 32 * RI + r) * 4;
-    const int b_sc_off = kScalesB + 4 * h * kScaleBlockStride + (wn * 32 * CJ + r) * 4;
-    struct BlockStep {  // a lane's operands of 16 elements per row
-        u32x2 ca[RI], cb[CJ];
-        uint32_t sa[RI], sb[CJ];
-    };
-    struct Frags {
-        f16x8_t a[RI], b[CJ];
-    };
-    auto read_bs = [&](BlockStep& s, const uint8_t* base, int b) __attribute__((always_inline)) {
+// A wave's results to C.  Stored from the accumulators an instruction writes 64-byte
+// pieces of rows (bf16; 128 in fp32), and that bounds wide and short products; so
+// each 32 rows pass through this wave's part of the staging buffers, which no one
+// needs any more, and leave in 16 bytes per lane, whole rows of the wave's tile at a
+// time: 1.07 GB of bf16 stored alone FIGURE.  Where rows of C do not begin at
+// multiples of 16 bytes they are stored directly.  Returns the largest magnitude of
+// what bf16 stores hold; rows and columns past the tile repeat its last ones, so
+// they need no exception.
+template <typename L, int RI, int CJ, typename OUT>
+__device__ __forceinline__ uint32_t store_tile(const f32x16_t (&acc)[RI][CJ], const Tile& t, uint8_t* smem, OUT* C,
+                                               int64_t N, int wm, int wn) {
+    constexpr int kPer = 16 / sizeof(OUT), kLanes = 32 * CJ / kPer;  // results per lane, lanes per row
+    constexpr int kStride = 32 * CJ * sizeof(OUT) + (sizeof(OUT) == 4 ? 32 : 16);  // rows 4 apart on other banks
+    static_assert(32 * kStride <= L::kWave, "32 rows fit a wave's part");
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+    uint8_t* mine = smem + (threadIdx.x >> 6) * L::kWave;
+    const int row0 = wm * 32 * RI, col0 = wn * 32 * CJ;
+    uint32_t tmax = 0u;
+    C += t.c;
+    if (N % kPer == 0) {
 #pragma unroll
         for (int i = 0; i < RI; ++i) {
-            s.ca[i] = *reinterpret_cast<const u32x2*>(base + a_code_off + i * 32 * kCodeStride + 8 * b);
-            s.sa[i] = *reinterpret_cast<const uint32_t*>(base + a_sc_off + b * kScaleBlockStride + i * 128);
-        }
 #pragma unroll
-        for (int j = 0; j < CJ; ++j) {
-            s.cb[j] = *reinterpret_cast<const u32x2*>(base + b_code_off + j * 32 * kCodeStride + 8 * b);
-            s.sb[j] = *reinterpret_cast<const uint32_t*>(base + b_sc_off + b * kScaleBlockStride + j * 128);
+            for (int e = 0; e < 16; ++e)
+#pragma unroll
+                for (int j = 0; j < CJ; ++j)
+                    put(*reinterpret_cast<OUT*>(mine + (8 * (e >> 2) + 4 * h + (e & 3)) * kStride + (32 * j + r) * sizeof(OUT)),
+                        (acc[i][j][e] * t.sa256) * t.sb, tmax);
+            wave_sync();
+#pragma unroll
+            for (int m = 0; m < 32 * kLanes / 64; ++m) {
+                const int row = m * (64 / kLanes) + lane / kLanes, col = lane % kLanes * kPer;
+                const u32x4 v = *reinterpret_cast<const u32x4*>(mine + row * kStride + col * sizeof(OUT));
+                if (row0 + 32 * i + row < t.rows && col0 + col < t.cols)
+                    *reinterpret_cast<u32x4*>(C + (row0 + 32 * i + row) * N + col0 + col) = v;
+            }
+            wave_sync();
         }
+        return tmax;
+    }
+#pragma unroll
+    for (int i = 0; i < RI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int row = row0 + i * 32 + 8 * (e >> 2) + 4 * h + (e & 3);
+#pragma unroll
+            for (int j = 0; j < CJ; ++j)
+                if (row < t.rows && col0 + r + 32 * j < t.cols)
+                    put(C[row * N + col0 + r + 32 * j], (acc[i][j][e] * t.sa256) * t.sb, tmax);
+        }
+    return tmax;
+}
+
+// 16 (4) bytes per lane from base + off straight to LDS, lane l's at lds + 16 l (4
+// l).  In assembly, because the compiler would wait for them at every later LDS read;
+// it knows neither the load nor when it ends: step_ready() does.  The s_nop is the
+// wait that the load needs behind a vector instruction's write of its scalar base and
+// behind that of m0, an output here because a clobber of it says nothing.
+__device__ __forceinline__ void load_to_lds16(const uint8_t* base, uint32_t off, uint32_t lds) {
+    uint32_t m0;
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %2, %3"
+                 : "=&{m0}"(m0)
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base)
+                 : "memory");
+}
+__device__ __forceinline__ void load_to_lds4(const uint8_t* base, uint32_t off, uint32_t lds) {
+    uint32_t m0;
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dword %2, %3"
+                 : "=&{m0}"(m0)
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base)
+                 : "memory");
+}
+// This wave's loads have landed and its LDS reads are done; behind the barrier that
+// holds for all waves: the step can be read, and the one before it overwritten.
+__device__ __forceinline__ void step_ready() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// LDS of a workgroup with tiles of up to BM x 128: two steps of codes (64 bytes a
+// row) and scale bytes (8 a row), and the table of expanded scales.
+constexpr int kBN = 128;
+template <int BM>
+struct Lds {
+    static_assert(BM >= 128, "4 waves bring the scales of 128 rows together");
+    static constexpr int kCodesA = 0, kCodesB = BM * 64, kScalesA = kCodesB + kBN * 64, kScalesB = kScalesA + BM * 8;
+    static constexpr int kStage = kScalesB + kBN * 8, kLut = 2 * kStage, kBytes = kLut + 1024;
+    static constexpr int kWave = 32 * (64 * 4 + 32);  // a wave's part of it in the epilogue
+    static_assert(4 * kWave <= kBytes, "the epilogue has room");
+};
+
+// rows of codes begin at multiples of 8 bytes, rows of scales anywhere
+typedef u32x4 u32x4_at8 __attribute__((aligned(8)));
+typedef u32x2 u32x2_at1 __attribute__((aligned(1)));
+
+// One step of a row where K is no multiple of 128: the 16-byte unit `unit` of its
+// codes, or its 8 scale bytes.  In a step that K cuts short blocks are clamped into
+// the row, and blocks past K get the scale 0, whose factor m = 0 makes every code 0.
+__device__ __forceinline__ u32x4 load_unit(const uint8_t* row, int64_t K, int64_t k0, int unit) {
+    if (k0 + kBK <= K) return *reinterpret_cast<const u32x4_at8*>(row + k0 / 2 + 16 * unit);
+    const int64_t ka = min(k0 + 32 * unit, K - 16), kb = min(k0 + 32 * unit + 16, K - 16);
+    const u32x2 x = *reinterpret_cast<const u32x2*>(row + ka / 2);
+    const u32x2 y = *reinterpret_cast<const u32x2*>(row + kb / 2);
+    return u32x4{x.x, x.y, y.x, y.y};
+}
+__device__ __forceinline__ u32x2 load_scales(const uint8_t* row, int64_t K, int64_t k0) {
+    const int64_t b0 = k0 / 16, blocks = K / 16;
+    if (b0 + 8 <= blocks) return *reinterpret_cast<const u32x2_at1*>(row + b0);
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t v = row[min(b0 + j, blocks - 1)];
+        w[j >> 2] |= (b0 + j < blocks ? v : 0u) << (8 * (j & 3));
+    }
+    return u32x2{w[0], w[1]};
+}
+
+// One tile of 32 RI WM rows x 128 columns, by WM x WN waves of RI x CJ 32 x 32
+// results.
+//
+// A step's codes stand in LDS row by row, 64 bytes each, 16-byte unit u of row i at u
+// ^ (i / 4 % 4), so that 16 lanes read a unit of 16 rows without bank conflicts.
+// They come straight from memory, a step ahead of the one that is multiplied, where
+// K is a multiple of 128 (DIRECT); else through registers, since rows are not
+// aligned then and the last step is masked.
+//
+// Lane (r, h) = (lane % 32, lane / 32) owns elements [64 h, 64 h + 64) of a row's
+// step: 2 units, 4 blocks, 8 matrix instructions.  A and B agree on it, so the sums
+// are those of the plain order.  A scale byte is expanded where it is used: 16 rows'
+// bytes mostly name few table entries.
+template <int BM, int RI, int CJ, int WM, int WN, bool DIRECT>
+__device__ __forceinline__ void compute_tile(const Tile& t, uint8_t* smem, const GemmGroupedArgs& g) {
+    using L = Lds<BM>;
+    constexpr int kRowsA = 32 * RI * WM;
+    static_assert(32 * CJ * WN == kBN && kRowsA <= BM && WM * WN == 4, "4 waves, 128 columns");
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int r = lane & 31, h = lane >> 5;
+    const int steps = __builtin_amdgcn_readfirstlane((int)((t.K + kBK - 1) / kBK));
+    const uint32_t* lut = reinterpret_cast<const uint32_t*>(smem + L::kLut);
+
+    // ---- staging: turn i of a wave brings the codes of rows 16 (wave + 4 i) .. + 15
+    // (4 lanes a row) and the scales of rows 32 (wave + 4 i) .. + 31 (2 lanes a row);
+    // rows past the tile repeat its last one, their results are not stored.  Offsets
+    // fit 32 bits: 256 rows of less than 2^23 bytes.
+    constexpr int kCodeTurnsA = (kRowsA + 63) / 64, kCodeTurnsB = kBN / 64, kScaleTurnsA = (kRowsA + 127) / 128;
+    uint32_t oa[kCodeTurnsA], ob[kCodeTurnsB], osa[kScaleTurnsA], osb;
+    const int code_row = 16 * wave + (lane >> 2), scale_row = 32 * wave + (lane >> 1);
+    const uint32_t unit = (lane & 3) ^ ((code_row >> 2) & 3);  // rows 64 apart have the same
+#pragma unroll
+    for (int i = 0; i < kCodeTurnsA; ++i) oa[i] = (uint32_t)min(code_row + 64 * i, t.rows - 1) * (uint32_t)t.a_stride;
+#pragma unroll
+    for (int i = 0; i < kCodeTurnsB; ++i) ob[i] = (uint32_t)min(code_row + 64 * i, t.cols - 1) * (uint32_t)t.b_stride;
+#pragma unroll
+    for (int i = 0; i < kScaleTurnsA; ++i) osa[i] = (uint32_t)min(scale_row + 128 * i, t.rows - 1) * (uint32_t)t.as_stride;
+    osb = (uint32_t)min(scale_row, t.cols - 1) * (uint32_t)t.bs_stride;
+    const uint8_t *a = t.a, *as = t.as, *b = t.b, *bs = t.bs;  // scalar: so are all of a tile's values
+    const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
+    auto stage = [&](int step, int at) __attribute__((always_inline)) {
+        const uint32_t to = lds + at * L::kStage;
+        const int64_t c = (int64_t)step * (kBK / 2), s = (int64_t)step * (kBK / 16);
+#pragma unroll
+        for (int i = 0; i < kCodeTurnsA; ++i)
+            load_to_lds16(a + c, oa[i] + 16 * unit, to + L::kCodesA + 1024 * (wave + 4 * i));
+#pragma unroll
+        for (int i = 0; i < kCodeTurnsB; ++i) load_to_lds16(b + c, ob[i] + 16 * unit, to + L::kCodesB + 1024 * (wave + 4 * i));
+#pragma unroll
+        for (int i = 0; i < kScaleTurnsA; ++i)
+            load_to_lds4(as + s, osa[i] + 4 * (lane & 1), to + L::kScalesA + 256 * (wave + 4 * i));
+        load_to_lds4(bs + s, osb + 4 * (lane & 1), to + L::kScalesB + 256 * wave);
     };
-    auto dequant = [&](Frags& f, const BlockStep& s, int half) __attribute__((always_inline)) {
+    u32x4 ra[kCodeTurnsA], rb[kCodeTurnsB];
+    u32x2 rsa[kScaleTurnsA], rsb;
+    auto fetch = [&](int step) __attribute__((always_inline)) {
+        const int64_t k0 = (int64_t)step * kBK;
 #pragma unroll
-        for (int i = 0; i < RI; ++i) f.a[i] = dequant8(half ? s.ca[i].y : s.ca[i].x, s.sa[i]);
+        for (int i = 0; i < kCodeTurnsA; ++i) ra[i] = load_unit(a + oa[i], t.K, k0, unit);
 #pragma unroll
-        for (int j = 0; j < CJ; ++j) f.b[j] = dequant8(half ? s.cb[j].y : s.cb[j].x, s.sb[j]);
+        for (int i = 0; i < kCodeTurnsB; ++i) rb[i] = load_unit(b + ob[i], t.K, k0, unit);
+#pragma unroll
+        for (int i = 0; i < kScaleTurnsA; ++i) rsa[i] = load_scales(as + osa[i], t.K, k0);
+        rsb = load_scales(bs + osb, t.K, k0);
+    };
+    auto put_stage = [&](int at) __attribute__((always_inline)) {
+        uint8_t* to = smem + at * L::kStage;
+#pragma unroll
+        for (int i = 0; i < kCodeTurnsA; ++i)
+            *reinterpret_cast<u32x4*>(to + L::kCodesA + 1024 * (wave + 4 * i) + 16 * lane) = ra[i];
+#pragma unroll
+        for (int i = 0; i < kCodeTurnsB; ++i) *reinterpret_cast<u32x4*>(to + L::kCodesB + 1024 * (wave + 4 * i) + 16 * lane) = rb[i];
+#pragma unroll
+        for (int i = 0; i < kScaleTurnsA; ++i)
+            *reinterpret_cast<uint32_t*>(to + L::kScalesA + 256 * (wave + 4 * i) + 4 * lane) = lane & 1 ? rsa[i].y : rsa[i].x;
+        *reinterpret_cast<uint32_t*>(to + L::kScalesB + 256 * wave + 4 * lane) = lane & 1 ? rsb.y : rsb.x;
     };
 
+    const int row_a = wm * 32 * RI + r, row_b = wn * 32 * CJ + r;
+    const int swizzle_a = (row_a >> 2) & 3, swizzle_b = (row_b >> 2) & 3;  // rows 32 apart have the same
     f32x16_t acc[RI][CJ];
 #pragma unroll
     for (int i = 0; i < RI; ++i)
@@ -257,104 +317,94 @@ __device__ __forceinline__ void compute_tile(const Tile& t, uint8_t* smem, void*
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-    if (nchunks > 0) {
-        gload(0);
-        lut_fetch();
-        lstore_codes(smem);
-        lstore_scales(smem);
-        gload(min(1, nchunks - 1));
-        __syncthreads();
-
-        BlockStep bsr[2];
-        Frags fr[2];
-        read_bs(bsr[0], smem, 0);
-        dequant(fr[0], bsr[0], 0);
-
-        for (int c = 0; c < nchunks; ++c) {
-            uint8_t* cur = smem + (c & 1) * kStage;
-            uint8_t* nxt = smem + ((c + 1) & 1) * kStage;
-#pragma unroll
-            for (int J = 0; J < 8; ++J) {
-                const Frags& f = fr[J & 1];
-#pragma unroll
-                for (int i = 0; i < RI; ++i)
-#pragma unroll
-                    for (int j = 0; j < CJ; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
-                if (J == 0 || J == 2 || J == 4) read_bs(bsr[((J >> 1) + 1) & 1], cur, (J >> 1) + 1);
-                if (J == 6) read_bs(bsr[0], nxt, 0);
-                if (J == 1) {
-                    lstore_codes(nxt);
-                    lut_fetch();
-                    gload(min(c + 2, nchunks - 1));
-                }
-                if (J == 2) lstore_scales(nxt);
-                dequant(fr[(J + 1) & 1], bsr[((J + 1) >> 1) & 1], (J + 1) & 1);
-                // each matrix instruction followed by its share of the rest
-                constexpr int kMfmas = RI * CJ, kValu = 8 * (RI + CJ) / kMfmas + 1, kPer = 16 / kMfmas;
-#pragma unroll
-                for (int q = 0; q < kMfmas; ++q) {
-                    __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(kSchedValu, kValu, 0);
-                    if (q * kPer < 10) __builtin_amdgcn_sched_group_barrier(kSchedDs, 2 * kPer, 0);
-                    if (q * kPer < 8) __builtin_amdgcn_sched_group_barrier(kSchedVmemRead, 2 * kPer, 0);
-                }
-                if (J == 5) __syncthreads();
-            }
+    if (steps > 0) {
+        if constexpr (DIRECT) {
+            stage(0, 0);
+        } else {
+            fetch(0);
+            put_stage(0);
         }
     }
+    for (int step = 0; step < steps; ++step) {
+        const uint8_t* cur = smem + (step & 1) * L::kStage;
+        step_ready();
+        if (step + 1 < steps) {
+            if constexpr (DIRECT) stage(step + 1, (step + 1) & 1);
+            else fetch(step + 1);
+        }
+        uint32_t sa[RI], sb[CJ];
+#pragma unroll
+        for (int i = 0; i < RI; ++i) sa[i] = *reinterpret_cast<const uint32_t*>(cur + L::kScalesA + (row_a + 32 * i) * 8 + 4 * h);
+#pragma unroll
+        for (int j = 0; j < CJ; ++j) sb[j] = *reinterpret_cast<const uint32_t*>(cur + L::kScalesB + (row_b + 32 * j) * 8 + 4 * h);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            u32x4 ca[RI], cb[CJ];
+#pragma unroll
+            for (int i = 0; i < RI; ++i)
+                ca[i] = *reinterpret_cast<const u32x4*>(cur + L::kCodesA + (row_a + 32 * i) * 64 + 16 * ((2 * h + p) ^ swizzle_a));
+#pragma unroll
+            for (int j = 0; j < CJ; ++j)
+                cb[j] = *reinterpret_cast<const u32x4*>(cur + L::kCodesB + (row_b + 32 * j) * 64 + 16 * ((2 * h + p) ^ swizzle_b));
+#pragma unroll
+            for (int block = 0; block < 2; ++block) {
+                uint32_t ea[RI], eb[CJ];
+#pragma unroll
+                for (int i = 0; i < RI; ++i) ea[i] = lut[(sa[i] >> (8 * (2 * p + block))) & 0xFFu];
+#pragma unroll
+                for (int j = 0; j < CJ; ++j) eb[j] = lut[(sb[j] >> (8 * (2 * p + block))) & 0xFFu];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    f16x8_t fa[RI], fb[CJ];
+#pragma unroll
+                    for (int i = 0; i < RI; ++i) fa[i] = dequant8(ca[i][2 * block + s], ea[i]);
+#pragma unroll
+                    for (int j = 0; j < CJ; ++j) fb[j] = dequant8(cb[j][2 * block + s], eb[j]);
+#pragma unroll
+                    for (int i = 0; i < RI; ++i)
+#pragma unroll
+                        for (int j = 0; j < CJ; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+                }
+            }
+        }
+        if constexpr (!DIRECT)
+            if (step + 1 < steps) put_stage((step + 1) & 1);
+    }
+    step_ready();  // all waves are past their last step: the stages are free
 
     // Epilogue: accumulator e of lane (r, h) is row 8 (e / 4) + 4 h + e % 4, column
     // r of its 32 x 32 tile.
-    const int row0 = wm * 32 * RI + 4 * h, col0 = wn * 32 * CJ + r;
-    const bool whole = t.rows == kRows && t.cols == kBN;
-    float* C = (float*)cptr + t.c;
-    uint16_t* Cb = (uint16_t*)cptr + t.c;
     uint32_t tmax = 0u;
-#pragma unroll
-    for (int i = 0; i < RI; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int row = row0 + i * 32 + 8 * (e >> 2) + (e & 3);
-            const int64_t off = row * N + col0;
-#pragma unroll
-            for (int j = 0; j < CJ; ++j) {
-                if (whole || (row < t.rows && col0 + 32 * j < t.cols)) {
-                    const float v = (acc[i][j][e] * t.sa256) * t.sb;
-                    if (c_bf16) {
-                        const uint16_t b = to_bf16(v);
-                        Cb[off + j * 32] = b;
-                        tmax = max(tmax, (uint32_t)(b & 0x7FFFu));
-                    } else {
-                        C[off + j * 32] = v;
-                    }
-                }
-            }
-        }
-    if (amax) amax_commit(tmax, amax);
+    if (g.c_bf16) tmax = store_tile<L, RI, CJ, uint16_t>(acc, t, smem, (uint16_t*)g.c, g.N, wm, wn);
+    else store_tile<L, RI, CJ, float>(acc, t, smem, (float*)g.c, g.N, wm, wn);
+    if (g.amax) amax_commit(tmax, g.amax);
 }
 
-template <bool ALIGNED>
+template <int BM, bool DIRECT>
 __device__ __forceinline__ void compute(const Tile& t, uint8_t* smem, const GemmGroupedArgs& g) {
-    if (t.rows > 128) compute_tile<4, 4, 2, 2, ALIGNED>(t, smem, g.c, g.c_bf16, g.N, g.amax);
-    else if (t.rows > 64) compute_tile<4, 2, 1, 4, ALIGNED>(t, smem, g.c, g.c_bf16, g.N, g.amax);
-    else if (t.rows > 32) compute_tile<2, 2, 1, 4, ALIGNED>(t, smem, g.c, g.c_bf16, g.N, g.amax);
-    else compute_tile<1, 2, 1, 4, ALIGNED>(t, smem, g.c, g.c_bf16, g.N, g.amax);
+    if constexpr (BM == 256) {
+        if (t.rows > 128) return compute_tile<BM, 4, 2, 2, 2, DIRECT>(t, smem, g);
+    }
+    if (t.rows > 64) compute_tile<BM, 2, 2, 2, 2, DIRECT>(t, smem, g);
+    else if (t.rows > 32) compute_tile<BM, 1, 2, 2, 2, DIRECT>(t, smem, g);
+    else compute_tile<BM, 1, 1, 1, 4, DIRECT>(t, smem, g);
 }
 
 // Consecutive workgroups go to the 8 XCDs in turn: each takes a contiguous range
 // of the n tiles, so that an L2 holds what its workgroups share.
-__device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t n) {
-    const int64_t per_xcd = n / 8;
+template <typename T>
+__device__ __forceinline__ T xcd_order(T id, T n) {
+    const T per_xcd = n / 8;
     return id < per_xcd * 8 ? (id % 8) * per_xcd + id / 8 : id;  // the tail keeps its number
 }
 
 // Tile l of a tiles_m x tiles_n rectangle, kGroupM tile rows at a time.
-__device__ __forceinline__ void tile_of(int64_t l, int64_t tiles_m, int64_t tiles_n, int64_t& tm, int64_t& tn) {
-    const int64_t width = kGroupM * tiles_n, first_m = l / width * kGroupM;
-    const int64_t rows = min(tiles_m - first_m, (int64_t)kGroupM);
-    tm = first_m + l % width % rows;
-    tn = l % width / rows;
+__device__ __forceinline__ void tile_of(uint32_t l, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm, uint32_t& tn) {
+    const uint32_t width = kGroupM * tiles_n, band = l / width, in = l - band * width;
+    const uint32_t rows = min(tiles_m - band * kGroupM, (uint32_t)kGroupM);
+    tn = in / rows;
+    tm = band * kGroupM + in - tn * rows;
 }
 
 // Expert of tile number id of fprop and dgrad, its rows, and the tile's number
@@ -362,69 +412,71 @@ __device__ __forceinline__ void tile_of(int64_t l, int64_t tiles_m, int64_t tile
 // rows).  Every wave finds it for itself, 64 experts at a time.
 struct Found {
     int g, begin, end;
-    int64_t full_tile, tn;
+    bool full;
+    uint32_t tile;  // number of a full tile among the expert's, or column tile
 };
-__device__ __forceinline__ int full_tiles(int len) { return (len + kBM / 2 - 1) / kBM; }
+template <int SIZE>
+__device__ __forceinline__ int full_tiles(int len) { return (len + SIZE / 2 - 1) / SIZE; }
 
-__device__ __forceinline__ bool find_tile(const GemmGroupedArgs& a, int64_t id, int64_t tiles_n, Found& f) {
+// Tile numbers fit 32 bits: experts * N * K < 2^40 and K >= 16 where there are any.
+template <int SIZE>
+__device__ __forceinline__ bool find_tile(const GemmGroupedArgs& a, uint32_t id, uint32_t tiles_n, Found& f) {
     const int lane = threadIdx.x & 63;
-    int64_t full = 0, rest = 0;  // row tiles of each kind
+    uint32_t full = 0, rest = 0;  // row tiles of each kind
+    GroupRows r{0, 0};
+    int n = 0;
+    bool more = false;
+    auto look = [&](int base) __attribute__((always_inline)) {
+        r = GroupRows{0, 0};
+        if (base + lane < a.experts) r = group_rows(a.offsets, base + lane, (int)a.rows);
+        n = full_tiles<SIZE>(r.end - r.begin);
+        more = r.end - r.begin > n * SIZE;
+    };
+    uint32_t upto = 0;
     for (int base = 0; base < a.experts; base += 64) {
-        int n = 0;
-        bool more = false;
-        if (base + lane < a.experts) {
-            const GroupRows r = group_rows(a.offsets, base + lane, (int)a.rows);
-            n = full_tiles(r.end - r.begin);
-            more = r.end - r.begin > (int64_t)n * kBM;
-        }
-        full += __shfl(wave_scan(n), 63);
+        look(base);
+        upto = wave_scan(n);
+        full += __shfl((int)upto, 63);
         rest += __popcll(__ballot(more));
     }
-    const bool in_full = id < full * tiles_n;
-    int64_t j = in_full ? id : id - full * tiles_n;
-    if (!in_full && j >= rest * tiles_n) return false;
-    j = xcd_order(j, (in_full ? full : rest) * tiles_n);
-    int64_t before = 0;  // row tiles of this kind before `base`
+    f.full = id < full * tiles_n;
+    uint32_t j = f.full ? id : id - full * tiles_n;
+    if (!f.full && j >= rest * tiles_n) return false;
+    j = xcd_order(j, (f.full ? full : rest) * tiles_n);
+    const uint32_t at = j / tiles_n;  // row tile of this kind
+    uint32_t before = 0;
     for (int base = 0; base < a.experts; base += 64) {
-        GroupRows r{0, 0};
-        int n = 0;
-        if (base + lane < a.experts) {
-            r = group_rows(a.offsets, base + lane, (int)a.rows);
-            n = full_tiles(r.end - r.begin);
-            if (!in_full) n = r.end - r.begin > (int64_t)n * kBM;
-        }
-        const int upto = wave_scan(n);
-        const uint64_t votes = __ballot((before + upto) * tiles_n > j);
+        if (a.experts > 64) look(base);  // else still there
+        if (!f.full) n = more;
+        if (!f.full || a.experts > 64) upto = wave_scan(n);
+        const uint64_t votes = __ballot(before + upto > at);
         if (votes) {
-            const int l = __builtin_ctzll(votes);  // the first expert that reaches beyond j
+            const int l = __builtin_ctzll(votes);  // the first expert that reaches beyond
             f.g = base + l;
             f.begin = __shfl(r.begin, l);
             f.end = __shfl(r.end, l);
-            const int64_t local = j - (before + __shfl(upto - n, l)) * tiles_n;
-            f.full_tile = in_full ? local : -1;
-            f.tn = in_full ? 0 : local;
+            f.tile = j - (before + __shfl((int)upto - n, l)) * tiles_n;
             return true;
         }
-        before += __shfl(upto, 63);
+        before += __shfl((int)upto, 63);
     }
     return false;
 }
 
-template <bool ALIGNED>
-__global__ __launch_bounds__(kThreads, 1) void gemm_grouped_nt_kernel(GemmGroupedArgs g) {
-    __shared__ __align__(16) uint8_t smem[kSmem];
+template <int BM, bool DIRECT>
+__global__ __launch_bounds__(kThreads, 2) void gemm_grouped_nt_kernel(GemmGroupedArgs g) {
+    using L = Lds<BM>;
+    __shared__ __align__(16) uint8_t smem[L::kBytes];
     Found f;
-    const int64_t tiles_n = (g.N + kBN - 1) / kBN;
-    if (!find_tile(g, g.first + blockIdx.x, tiles_n, f)) return;
-    reinterpret_cast<uint32_t*>(smem + kLut)[threadIdx.x] = expand_scale(threadIdx.x);
+    const uint32_t tiles_n = (uint32_t)((g.N + kBN - 1) / kBN);
+    if (!find_tile<BM>(g, (uint32_t)g.first + blockIdx.x, tiles_n, f)) return;
+    reinterpret_cast<uint32_t*>(smem + L::kLut)[threadIdx.x] = expand_scale(threadIdx.x);
     const int expert = __builtin_amdgcn_readfirstlane(f.g);
     const int begin = __builtin_amdgcn_readfirstlane(f.begin), end = __builtin_amdgcn_readfirstlane(f.end);
-    const int full = full_tiles(end - begin);
-    int64_t tm = full, tn = f.tn;
-    if (f.full_tile >= 0) tile_of(f.full_tile, full, tiles_n, tm, tn);
-    tm = __builtin_amdgcn_readfirstlane((int)tm);
-    tn = __builtin_amdgcn_readfirstlane((int)tn);
-    const int64_t m0 = begin + tm * kBM, n0 = tn * kBN;
+    const int full = full_tiles<BM>(end - begin);
+    uint32_t tm = full, tn = __builtin_amdgcn_readfirstlane(f.tile);
+    if (__builtin_amdgcn_readfirstlane(f.full)) tile_of(tn, full, tiles_n, tm, tn);
+    const int64_t m0 = begin + (int64_t)tm * BM, n0 = (int64_t)tn * kBN;
     Tile t;
     t.a_stride = t.b_stride = g.K / 2;
     t.as_stride = t.bs_stride = g.K / 16;
@@ -433,26 +485,31 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_grouped_nt_kernel(GemmGroupe
     t.as = g.a_scales + m0 * t.as_stride;
     t.b = g.b_codes + (expert * g.N + n0) * t.b_stride;
     t.bs = g.b_scales + (expert * g.N + n0) * t.bs_stride;
-    t.rows = (int)min(end - m0, (int64_t)kBM);
+    t.rows = (int)min(end - m0, (int64_t)BM);
     t.cols = (int)min(g.N - n0, (int64_t)kBN);
     t.c = m0 * g.N + n0;
     t.sa256 = *g.a_ts * 256.0f;
     t.sb = g.b_ts[expert * g.b_ts_step];
-    __syncthreads();  // scale table visible
-    compute<ALIGNED>(t, smem, g);
+    compute<BM, DIRECT>(t, smem, g);
 }
 
-__global__ __launch_bounds__(kThreads, 1) void gemm_grouped_wgrad_kernel(GemmGroupedArgs g) {
-    __shared__ __align__(16) uint8_t smem[kSmem];
-    reinterpret_cast<uint32_t*>(smem + kLut)[threadIdx.x] = expand_scale(threadIdx.x);
-    const int64_t tiles_m = (g.M + kBM - 1) / kBM, tiles_n = (g.N + kBN - 1) / kBN;
-    const int64_t j = xcd_order(g.first + blockIdx.x, g.experts * tiles_m * tiles_n);
-    const int expert = (int)(j / (tiles_m * tiles_n));
-    int64_t tm, tn;
-    tile_of(j % (tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
-    const GroupRows own = group_rows(g.offsets, expert, (int)g.rows);
+template <int BM>
+__global__ __launch_bounds__(kThreads, 2) void gemm_grouped_wgrad_kernel(GemmGroupedArgs g) {
+    using L = Lds<BM>;
+    __shared__ __align__(16) uint8_t smem[L::kBytes];
+    reinterpret_cast<uint32_t*>(smem + L::kLut)[threadIdx.x] = expand_scale(threadIdx.x);
+    const uint32_t tiles_m = (uint32_t)((g.M + BM - 1) / BM), tiles_n = (uint32_t)((g.N + kBN - 1) / kBN);
+    const int64_t j = xcd_order(g.first + blockIdx.x, (int64_t)g.experts * tiles_m * tiles_n);
+    const int expert = __builtin_amdgcn_readfirstlane((int)(j / (tiles_m * tiles_n)));
+    uint32_t tm, tn;
+    tile_of((uint32_t)(j - (int64_t)expert * (tiles_m * tiles_n)), tiles_m, tiles_n, tm, tn);
+    tm = __builtin_amdgcn_readfirstlane(tm);
+    tn = __builtin_amdgcn_readfirstlane(tn);
+    GroupRows own = group_rows(g.offsets, expert, (int)g.rows);
+    own.begin = __builtin_amdgcn_readfirstlane(own.begin);
+    own.end = __builtin_amdgcn_readfirstlane(own.end);
     const int64_t padded = 128 * ((g.rows + 127) / 128 + g.experts), p = padded_begin(own.begin, expert);
-    const int64_t m0 = tm * kBM, n0 = tn * kBN;
+    const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * kBN;
     Tile t;
     t.a_stride = t.b_stride = padded / 2;
     t.as_stride = t.bs_stride = padded / 16;
@@ -461,35 +518,52 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_grouped_wgrad_kernel(GemmGro
     t.as = g.a_scales + m0 * t.as_stride + p / 16;
     t.b = g.b_codes + n0 * t.b_stride + p / 2;
     t.bs = g.b_scales + n0 * t.bs_stride + p / 16;
-    t.rows = (int)min(g.M - m0, (int64_t)kBM);
+    t.rows = (int)min(g.M - m0, (int64_t)BM);
     t.cols = (int)min(g.N - n0, (int64_t)kBN);
     t.c = (expert * g.M + m0) * g.N + n0;
     t.sa256 = *g.a_ts * 256.0f;
     t.sb = *g.b_ts;
-    __syncthreads();  // scale table visible
-    compute<true>(t, smem, g);
+    compute<BM, true>(t, smem, g);
 }
+
+template <int BM, bool DIRECT>
+void launch_nt(GemmGroupedArgs g, hipStream_t stream) {
+    // an expert's rows make at most rows / BM tiles and one more
+    const int64_t row_tiles = g.rows / BM + (g.experts < g.rows ? g.experts : g.rows);
+    in_launches(row_tiles * ((g.N + kBN - 1) / kBN), kThreads, [&](int64_t first, dim3 grid) {
+        g.first = first;
+        hipLaunchKernelGGL((gemm_grouped_nt_kernel<BM, DIRECT>), grid, dim3(kThreads), 0, stream, g);
+    });
+}
+
+template <int BM>
+void launch_wgrad(GemmGroupedArgs g, hipStream_t stream) {
+    const int64_t tiles = g.experts * ((g.M + BM - 1) / BM) * ((g.N + kBN - 1) / kBN);
+    in_launches(tiles, kThreads, [&](int64_t first, dim3 grid) {
+        g.first = first;
+        hipLaunchKernelGGL(gemm_grouped_wgrad_kernel<BM>, grid, dim3(kThreads), 0, stream, g);
+    });
+}
+
+// 256 rows where that leaves work for two workgroups on each of the 256 CUs, else 128
+// (FIGURE).
+constexpr int64_t kFew = 512;
 
 }  // namespace
 
-void launch_gemm_grouped_nt(const GemmGroupedArgs& args, hipStream_t stream) {
-    GemmGroupedArgs g = args;
-    // an expert's rows make at most rows / 256 tiles and one more
-    const int64_t row_tiles = g.rows / kBM + (g.experts < g.rows ? g.experts : g.rows);
-    in_launches(row_tiles * ((g.N + kBN - 1) / kBN), kThreads, [&](int64_t first, dim3 grid) {
-        g.first = first;
-        if (g.K % kBK == 0) hipLaunchKernelGGL(gemm_grouped_nt_kernel<true>, grid, dim3(kThreads), 0, stream, g);
-        else hipLaunchKernelGGL(gemm_grouped_nt_kernel<false>, grid, dim3(kThreads), 0, stream, g);
-    });
+void launch_gemm_grouped_nt(const GemmGroupedArgs& g, hipStream_t stream) {
+    // rows of average experts: the tiles that 256 rows each make
+    const int64_t each = (g.rows + g.experts - 1) / g.experts;
+    const int64_t tiles = (g.experts < g.rows ? g.experts : g.rows) * ((each + 255) / 256) * ((g.N + kBN - 1) / kBN);
+    // through registers 256 rows spill, and steps take twice as long
+    if (g.K % kBK != 0) launch_nt<128, false>(g, stream);
+    else if (tiles >= kFew) launch_nt<256, true>(g, stream);
+    else launch_nt<128, true>(g, stream);
 }
 
-void launch_gemm_grouped_wgrad(const GemmGroupedArgs& args, hipStream_t stream) {
-    GemmGroupedArgs g = args;
-    const int64_t tiles = g.experts * ((g.M + kBM - 1) / kBM) * ((g.N + kBN - 1) / kBN);
-    in_launches(tiles, kThreads, [&](int64_t first, dim3 grid) {
-        g.first = first;
-        hipLaunchKernelGGL(gemm_grouped_wgrad_kernel, grid, dim3(kThreads), 0, stream, g);
-    });
+void launch_gemm_grouped_wgrad(const GemmGroupedArgs& g, hipStream_t stream) {
+    if (g.experts * ((g.M + 255) / 256) * ((g.N + kBN - 1) / kBN) >= kFew) launch_wgrad<256>(g, stream);
+    else launch_wgrad<128>(g, stream);
 }
 
 }  // namespace ue5m3fp4

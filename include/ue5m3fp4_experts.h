@@ -90,8 +90,8 @@ UE5M3FP4_API int ue5m3fp4_quantize_grouped(const uint16_t* x, int64_t x_rows, in
  *   c: [rows][N], bf16 (rounded to nearest even) or fp32;
  *   amax_inout: nullable, for bf16 outputs only (EINVAL): receives
  *       max(*amax_inout, max|C|) over the values stored (a NaN propagates).
- * K % 16 == 0 (ESHAPE); rows, N, K < 2^31, rows * N, rows * K and experts * N
- * * K < 2^40 (ERANGE).  c must not overlap the operands. */
+ * K % 16 == 0 (ESHAPE); rows, N < 2^31, K < 2^24, rows * N, rows * K and
+ * experts * N * K < 2^40 (ERANGE).  c must not overlap the operands. */
 UE5M3FP4_API int ue5m3fp4_gemm_grouped_nt(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_ts,
                                           const uint8_t* b_codes, const uint8_t* b_scales, const float* b_ts,
                                           int64_t b_ts_count, const int32_t* offsets, int64_t experts, int64_t rows,
@@ -102,8 +102,8 @@ UE5M3FP4_API int ue5m3fp4_gemm_grouped_nt(const uint8_t* a_codes, const uint8_t*
  *   C_g[i][j] = (tsA * tsB) * sum_p A(i, p) * B(j, p),  fp32 accumulation.
  *   a: M x rows_padded (dY's transposed output); b: N x rows_padded (X's);
  *   c: [experts][M][N], bf16 or fp32; an expert without rows gets zeros.
- * M, N, rows, rows_padded < 2^31; M * rows_padded, N * rows_padded and
- * experts * M * N < 2^40 (ERANGE). */
+ * M, N < 2^31, rows_padded < 2^24; M * rows_padded, N * rows_padded and experts
+ * * M * N < 2^40 (ERANGE). */
 UE5M3FP4_API int ue5m3fp4_gemm_grouped_wgrad(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_ts,
                                              const uint8_t* b_codes, const uint8_t* b_scales, const float* b_ts,
                                              const int32_t* offsets, int64_t experts, int64_t rows, int64_t M,

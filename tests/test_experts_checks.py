@@ -72,7 +72,7 @@ def test_gemm_argument_checks(L):
         assert gr(L, **{name: P + 2}) == EALIGN
     assert gr(L, am=P + 2) == EALIGN and gr(L, c=P + 4) == EALIGN
     assert gr(L, K=40) == ESHAPE
-    assert gr(L, rows=1 << 31) == ERANGE and gr(L, N=1 << 31) == ERANGE and gr(L, K=1 << 31) == ERANGE
+    assert gr(L, rows=1 << 31) == ERANGE and gr(L, N=1 << 31) == ERANGE and gr(L, K=1 << 24) == ERANGE
     assert gr(L, rows=1 << 20, N=1 << 20) == ERANGE and gr(L, E=65536, N=1 << 12, K=1 << 12) == ERANGE
     assert gr(L, E=65537) == ERANGE
     assert gr(L, E=0, n=0, off=None) == OK and gr(L, rows=0, c=None) == OK and gr(L, N=0, c=None) == OK
@@ -88,7 +88,7 @@ def test_wgrad_argument_checks(L):
     for name in ("ac", "as_", "at", "bc", "bs", "bt", "off", "c"):
         assert gw(L, **{name: None}) == EINVAL
         assert gw(L, **{name: P + 2}) == EALIGN
-    assert gw(L, rows=(1 << 31) - 128) == ERANGE and gw(L, M=1 << 31) == ERANGE and gw(L, E=65537) == ERANGE
+    assert gw(L, rows=(1 << 24) - 256) == ERANGE and gw(L, M=1 << 31) == ERANGE and gw(L, E=65537) == ERANGE
     assert gw(L, rows=1 << 20, M=1 << 20) == ERANGE and gw(L, E=65536, M=1 << 12, N=1 << 12) == ERANGE
     assert gw(L, E=0, off=None) == OK and gw(L, M=0) == OK and gw(L, N=0) == OK
 
@@ -106,7 +106,7 @@ def test_weight_only_argument_checks(L):
         assert wo(L, **{name: P + 2}) == EALIGN
     assert wo(L, off=P + 2) == EALIGN and wo(L, ldx=36) == EALIGN
     assert wo(L, K=40, ldx=40) == ESHAPE and wo(L, ldx=24) == ESHAPE and wo(L, ldo=31) == ESHAPE
-    assert wo(L, rows=1 << 31) == ERANGE and wo(L, ldx=1 << 39) == ERANGE and wo(L, ldo=1 << 39) == ERANGE
+    assert wo(L, rows=1 << 31) == ERANGE and wo(L, K=1 << 24, ldx=1 << 24) == ERANGE and wo(L, ldx=1 << 39) == ERANGE and wo(L, ldo=1 << 39) == ERANGE
     assert wo(L, E=65536, N=1 << 12, K=1 << 12) == ERANGE and wo(L, E=65537) == ERANGE
     assert wo(L, rows=0, out=None) == OK and wo(L, N=0, ldo=0) == OK and wo(L, E=0, n=0, off=None) == OK
 
