@@ -51,17 +51,29 @@ __device__ __forceinline__ int lds_offset(int row, int u) {
 }
 
 // Workgroup number -> tile: each XCD takes a contiguous range of an order that
-// runs down bands of 256 rows column by column, so that tiles which share lines
-// of the transposed codes meet in one L2.
+// runs down bands of 256 rows column by column, so that tiles which share lines of
+// the transposed codes meet in one L2.  The numbers fit 32 bits: cols * rows_padded
+// < 2^40, and a tile has 32 x 256 elements, or at least 32 rows.
 template <int TR>
-__device__ __forceinline__ void tile_of(int64_t j, int64_t tiles_r, int64_t tiles_c, int64_t& R0, int64_t& C0) {
-    constexpr int kBand = Shape<TR>::kBand;
-    const int64_t per_xcd = tiles_r * tiles_c / 8;
+__device__ __forceinline__ void tile_of(uint32_t j, uint32_t tiles_r, uint32_t tiles_c, int64_t& R0, int64_t& C0) {
+    constexpr uint32_t kBand = Shape<TR>::kBand;
+    const uint32_t per_xcd = tiles_r * tiles_c / 8;
     if (j < per_xcd * 8) j = (j % 8) * per_xcd + j / 8;  // the tail keeps its number
-    const int64_t band = j / (kBand * tiles_c), rem = j - band * kBand * tiles_c;
-    const int64_t h = min((int64_t)kBand, tiles_r - kBand * band);
-    C0 = rem / h * kTileCols;
-    R0 = (kBand * band + rem % h) * TR;
+    const uint32_t band = j / (kBand * tiles_c), rem = j - band * kBand * tiles_c;
+    const uint32_t h = min(kBand, tiles_r - kBand * band), column = rem / h;
+    C0 = (int64_t)column * kTileCols;
+    R0 = (int64_t)(kBand * band + rem - column * h) * TR;
+}
+
+// block_scale, which leaves tiny blocks under K < 1 to the general path, for a tile
+// whose last rows may be zeros: a zero block has code 0 and r = 0 there like any
+// other that flushes.  (Left to the general path, the last tiles of 16 experts' rows
+// made a call on 16384 x 4096 take 69 us instead of 48.)
+__device__ __forceinline__ BlockScale scale_of(uint32_t amax16, const Ctx& ctx, const float* rlut, bool& ok) {
+    bool fast = ctx.fastK;
+    const BlockScale b = block_scale(amax16, ctx, rlut, fast);
+    ok = ok & (fast | ((amax16 == 0u) & ctx.fastK));
+    return b;
 }
 
 // Largest magnitude (bf16 bits) of the workgroup folded into *amax: one atomic
@@ -80,7 +92,10 @@ __device__ __forceinline__ void amax_commit(uint32_t m, float* amax) {
     }
 }
 
-template <int TR, bool ROW, bool COL, bool SR>
+// W32: every call number of the stochastic rounding is below 2^32, so the counter's
+// second word is 0 and the half of the first rounds that depends on it is the same in
+// all lanes.  ONCE: no index, so each row is read once, past the caches.
+template <int TR, bool ROW, bool COL, bool SR, bool W32, bool ONCE>
 __global__ __launch_bounds__(kThreads) void quantize_grouped_kernel(QuantizeGroupedArgs a, int64_t first) {
     using S = Shape<TR>;
     constexpr int kRowsPerThread = S::kRowsPerThread, kRowBlocks = S::kRowBlocks, kPairsPerWave = S::kPairsPerWave;
@@ -89,64 +104,95 @@ __global__ __launch_bounds__(kThreads) void quantize_grouped_kernel(QuantizeGrou
     const int t = threadIdx.x, lane = t & 63;
     const int64_t padded = 128 * ((a.rows + 127) / 128 + a.experts);
     int64_t R0, C0;
-    tile_of<TR>(first + blockIdx.x, padded / TR, (a.cols + kTileCols - 1) / kTileCols, R0, C0);
+    tile_of<TR>((uint32_t)first + blockIdx.x, (uint32_t)(padded / TR), (uint32_t)((a.cols + kTileCols - 1) / kTileCols), R0, C0);
 
     // ---- the tile's expert, and the grouped rows [row0, end) it has here
+    const float ts = (ROW || COL) ? *a.tensor_scale : 0.0f;
     int g = -1;
+    GroupRows own{0, 0};
     for (int base = 0; base < a.experts; base += 64) {
+        GroupRows r{0, 0};
         bool before = false;
-        if (base + lane < a.experts)
-            before = padded_begin(group_rows(a.offsets, base + lane, (int)a.rows).begin, base + lane) <= R0;
+        if (base + lane < a.experts) {
+            r = group_rows(a.offsets, base + lane, (int)a.rows);
+            before = padded_begin(r.begin, base + lane) <= R0;
+        }
         const uint64_t votes = __ballot(before);
-        g += __popcll(votes);
-        if (votes != ~(uint64_t)0) break;
+        if (votes == 0) break;
+        const int last = __popcll(votes) - 1;
+        g = base + last;
+        own.begin = __shfl(r.begin, last);
+        own.end = __shfl(r.end, last);
+        if (last < 63) break;
     }
     if (g < 0) return;  // before the first expert's rows
-    const GroupRows own = group_rows(a.offsets, g, (int)a.rows);
     const int64_t rel = R0 - padded_begin(own.begin, g);
     const int64_t end = own.end, row0 = own.begin + rel;
     // behind the expert's padding (or, for the row-wise output alone, its rows);
     // before its first row only where the offsets decrease
     if (rel < 0 || (COL ? rel >= (end - own.begin + 127) / 128 * 128 : row0 >= end)) return;
 
+    // padding alone: zeros, unless the tensor scale makes a zero block NaN (0 / 0)
+    if (COL && row0 >= end && 6.0f * ts != 0.0f && ts == ts) {
+        const int column = t;
+        if (C0 + column < a.cols) {
+#pragma unroll
+            for (int k = 0; k < TR / 32; ++k)
+                *reinterpret_cast<u32x4*>(a.col_codes + (C0 + column) * (padded / 2) + R0 / 2 + 16 * k) = u32x4{0u, 0u, 0u, 0u};
+            *reinterpret_cast<uint32_t*>(a.col_scales + (C0 + column) * (padded / 16) + R0 / 16) = 0u;
+        }
+        return;
+    }
+
     // ---- loads: 16-byte unit u of tile rows rbase + 8k; rows that are not the
-    // expert's, or whose index is out of range, are zeros.  Addresses are
-    // clamped into x, so every load is unconditional.
+    // expert's, or whose index is out of range, are zeros.  Addresses are clamped
+    // into x, so every load is unconditional.
     const int u = t & 31, rbase = t >> 5;
     const int64_t c0 = C0 + 8 * u;
-    const bool col_ok = c0 < a.cols;
+    const bool col_ok = c0 < a.cols, interior = row0 + TR <= end && C0 + kTileCols <= a.cols;
     const uint16_t* src = a.x + (col_ok ? c0 : a.cols - 8);
     u32x4 w[kRowsPerThread];
-    bool valid[kRowsPerThread];
-    int64_t from[kRowsPerThread];
+    uint32_t zero = 0u;  // bit k: row k is not there
+    if (ONCE) {
+        if (interior) {  // one base address, then a stride common to the launch
+            src += (row0 + rbase) * a.ld;
 #pragma unroll
-    for (int k = 0; k < kRowsPerThread; ++k) {
-        const int64_t r = row0 + rbase + 8 * k;
-        valid[k] = r < end;
-        from[k] = min(r, a.rows - 1);
-    }
-    if (a.index) {
+            for (int k = 0; k < kRowsPerThread; ++k)
+                w[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(src + (int64_t)(8 * k) * a.ld));
+        } else {
 #pragma unroll
-        for (int k = 0; k < kRowsPerThread; ++k) from[k] = a.index[from[k]];
+            for (int k = 0; k < kRowsPerThread; ++k) {
+                const int64_t r = row0 + rbase + 8 * k;
+                if (r >= end) zero |= 1u << k;
+                w[k] = *reinterpret_cast<const u32x4*>(src + min(r, a.rows - 1) * a.ld);
+            }
+        }
+    } else {
+        int32_t from[kRowsPerThread];
+        const int32_t* index = a.index + row0 + rbase;
+#pragma unroll
+        for (int k = 0; k < kRowsPerThread; ++k) from[k] = index[interior ? 8 * k : min((int64_t)(8 * k), a.rows - 1 - row0 - rbase)];
 #pragma unroll
         for (int k = 0; k < kRowsPerThread; ++k) {
-            if (from[k] < 0 || from[k] >= a.x_rows) {
-                valid[k] = false;
+            if ((uint32_t)from[k] >= (uint32_t)a.x_rows || (!interior && row0 + rbase + 8 * k >= end)) {
+                zero |= 1u << k;
                 from[k] = 0;
             }
         }
-    }
-    if (a.x_rows > 0) {
+        if (a.x_rows > 0) {
 #pragma unroll
-        for (int k = 0; k < kRowsPerThread; ++k) w[k] = *reinterpret_cast<const u32x4*>(src + from[k] * a.ld);
+            for (int k = 0; k < kRowsPerThread; ++k) w[k] = *reinterpret_cast<const u32x4*>(src + (uint32_t)from[k] * a.ld);
+        }
     }
+    if (__any(zero)) {
 #pragma unroll
-    for (int k = 0; k < kRowsPerThread; ++k)
-        if (!valid[k]) w[k] = u32x4{0u, 0u, 0u, 0u};
+        for (int k = 0; k < kRowsPerThread; ++k)
+            if ((zero >> k) & 1u) w[k] = u32x4{0u, 0u, 0u, 0u};
+    }
 
     Ctx ctx{0.0f, 0.0f, 0.0f, false, false};
     if (ROW || COL) {
-        ctx = make_ctx(*a.tensor_scale);
+        ctx = make_ctx(ts);
         rlut[t] = rcp_entry<SR>((uint32_t)t, ctx.ts);
     }
 
@@ -176,7 +222,7 @@ __global__ __launch_bounds__(kThreads) void quantize_grouped_kernel(QuantizeGrou
         for (int m = 0; m < kRowsPerThread / 2; ++m) {
             const uint32_t mine = p ? hmax[2 * m + 1] : hmax[2 * m];
             const uint32_t other = p ? hmax[2 * m] : hmax[2 * m + 1];
-            const BlockScale b = block_scale(max(mine, swap_pair(other)), ctx, rlut, ok);
+            const BlockScale b = scale_of(max(mine, swap_pair(other)), ctx, rlut, ok);
             const uint32_t pc = swap_pair(b.code);
             const float pr = __uint_as_float(swap_pair(__float_as_uint(b.r)));
             code[2 * m] = p ? pc : b.code;
@@ -188,7 +234,8 @@ __global__ __launch_bounds__(kThreads) void quantize_grouped_kernel(QuantizeGrou
         const bool pair_ok = (ok_bit & swap_pair(ok_bit)) != 0u;  // one path for both lanes of a pair
         uint32_t packed[kRowsPerThread];
         auto words = [&](int k) {
-            return sr_words(((uint64_t)(row0 + rbase + 8 * k) * (uint64_t)a.cols + (uint64_t)c0) >> 3, a.offset, 0u, a.seed);
+            const uint64_t n = ((uint64_t)(row0 + rbase + 8 * k) * (uint64_t)a.cols + (uint64_t)c0) >> 3;
+            return W32 ? sr_words32((uint32_t)n, a.offset, 0u, a.seed) : sr_words(n, a.offset, 0u, a.seed);
         };
         if (__builtin_expect(pair_ok, 1)) {
 #pragma unroll
@@ -211,12 +258,22 @@ __global__ __launch_bounds__(kThreads) void quantize_grouped_kernel(QuantizeGrou
                 code[k] = b.code;
             }
         }
+        uint8_t* pc = a.row_codes + (row0 + rbase) * (a.cols / 2) + c0 / 2;
+        uint8_t* ps = a.row_scales + (row0 + rbase) * (a.cols / 16) + c0 / 16;
+        const int64_t cstep = 8 * (a.cols / 2), sstep = 8 * (a.cols / 16);
+        if (interior) {  // both lanes of a pair store the block's scale byte
 #pragma unroll
-        for (int k = 0; k < kRowsPerThread; ++k) {
-            const int64_t r = row0 + rbase + 8 * k;
-            if (col_ok && r < end) {
-                __builtin_nontemporal_store(packed[k], reinterpret_cast<uint32_t*>(a.row_codes + r * (a.cols / 2) + c0 / 2));
-                if (p == 0) a.row_scales[r * (a.cols / 16) + c0 / 16] = (uint8_t)code[k];
+            for (int k = 0; k < kRowsPerThread; ++k) {
+                __builtin_nontemporal_store(packed[k], reinterpret_cast<uint32_t*>(pc + k * cstep));
+                ps[k * sstep] = (uint8_t)code[k];
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kRowsPerThread; ++k) {
+                if (col_ok && row0 + rbase + 8 * k < end) {
+                    *reinterpret_cast<uint32_t*>(pc + k * cstep) = packed[k];
+                    if (p == 0) ps[k * sstep] = (uint8_t)code[k];
+                }
             }
         }
     }
@@ -238,16 +295,19 @@ __global__ __launch_bounds__(kThreads) void quantize_grouped_kernel(QuantizeGrou
 #pragma unroll
             for (int i = 0; i < 16; ++i) m2 = pk_max_u16(m2, cw[i] & 0x7FFF7FFFu);
             bool ok = ctx.fastK;
-            BlockScale ba = block_scale(m2 & 0xFFFFu, ctx, rlut, ok);
-            BlockScale bb = block_scale(m2 >> 16, ctx, rlut, ok);
+            BlockScale ba = scale_of(m2 & 0xFFFFu, ctx, rlut, ok);
+            BlockScale bb = scale_of(m2 >> 16, ctx, rlut, ok);
             U32x4 rnd[4];
             if (SR) {
                 const uint64_t na = ((uint64_t)ca * (uint64_t)padded + (uint64_t)r0) >> 3;
                 const uint64_t nb = na + (uint64_t)(padded >> 3);
-                rnd[0] = sr_words(na, a.offset, 1u, a.seed);
-                rnd[1] = sr_words(na + 1u, a.offset, 1u, a.seed);
-                rnd[2] = sr_words(nb, a.offset, 1u, a.seed);
-                rnd[3] = sr_words(nb + 1u, a.offset, 1u, a.seed);
+                auto words = [&](uint64_t n) {
+                    return W32 ? sr_words32((uint32_t)n, a.offset, 1u, a.seed) : sr_words(n, a.offset, 1u, a.seed);
+                };
+                rnd[0] = words(na);
+                rnd[1] = words(na + 1u);
+                rnd[2] = words(nb);
+                rnd[3] = words(nb + 1u);
             }
             uint32_t pa[2], pb[2];
             if (__builtin_expect(ok, 1)) {
@@ -278,7 +338,7 @@ __global__ __launch_bounds__(kThreads) void quantize_grouped_kernel(QuantizeGrou
                     pb[hh] = encode8_general<SR>(u32x4{lb[0], lb[1], lb[2], lb[3]}, bb.code, bb.r, rnd[2 + hh]);
                 }
             }
-            if (ca < a.cols) {  // columns come in pairs: cols % 16 == 0
+            if (interior || ca < a.cols) {  // columns come in pairs: cols % 16 == 0
                 *reinterpret_cast<u32x2*>(a.col_codes + ca * (padded / 2) + r0 / 2) = u32x2{pa[0], pa[1]};
                 *reinterpret_cast<u32x2*>(a.col_codes + (ca + 1) * (padded / 2) + r0 / 2) = u32x2{pb[0], pb[1]};
                 a.col_scales[ca * (padded / 16) + r0 / 16] = (uint8_t)ba.code;
@@ -289,12 +349,21 @@ __global__ __launch_bounds__(kThreads) void quantize_grouped_kernel(QuantizeGrou
     if (a.amax) amax_commit(tmax, a.amax);
 }
 
-template <int TR, bool ROW, bool COL, bool SR>
-void launch(const QuantizeGroupedArgs& a, hipStream_t stream) {
+template <int TR, bool ROW, bool COL, bool SR, bool W32, bool ONCE>
+void launch_as(const QuantizeGroupedArgs& a, hipStream_t stream) {
     const int64_t tiles = rows_padded(a.rows, a.experts) / TR * ((a.cols + kTileCols - 1) / kTileCols);
     in_launches(tiles, kThreads, [&](int64_t first, dim3 grid) {
-        hipLaunchKernelGGL((quantize_grouped_kernel<TR, ROW, COL, SR>), grid, dim3(kThreads), 0, stream, a, first);
+        hipLaunchKernelGGL((quantize_grouped_kernel<TR, ROW, COL, SR, W32, ONCE>), grid, dim3(kThreads), 0, stream, a, first);
     });
+}
+
+template <int TR, bool ROW, bool COL, bool SR>
+void launch(const QuantizeGroupedArgs& a, hipStream_t stream) {
+    if constexpr (SR) {
+        if (rows_padded(a.rows, a.experts) * a.cols < (int64_t)1 << 35)
+            return a.index ? launch_as<TR, ROW, COL, SR, true, false>(a, stream) : launch_as<TR, ROW, COL, SR, true, true>(a, stream);
+    }
+    a.index ? launch_as<TR, ROW, COL, SR, false, false>(a, stream) : launch_as<TR, ROW, COL, SR, false, true>(a, stream);
 }
 
 }  // namespace
