@@ -416,7 +416,7 @@ struct Found {
     uint32_t tile;  // number of a full tile among the expert's, or column tile
 };
 template <int SIZE>
-__device__ __forceinline__ int full_tiles(int len) { return (len + SIZE / 2 - 1) / SIZE; }
+__device__ __forceinline__ int full_tiles(int len) { return (int)(((uint32_t)len + (SIZE / 2 - 1)) / SIZE); }
 
 // Tile numbers fit 32 bits: experts * N * K < 2^40 and K >= 16 where there are any.
 template <int SIZE>
@@ -430,7 +430,7 @@ __device__ __forceinline__ bool find_tile(const GemmGroupedArgs& a, uint32_t id,
         r = GroupRows{0, 0};
         if (base + lane < a.experts) r = group_rows(a.offsets, base + lane, (int)a.rows);
         n = full_tiles<SIZE>(r.end - r.begin);
-        more = r.end - r.begin > n * SIZE;
+        more = (uint32_t)(r.end - r.begin) > (uint32_t)n * SIZE;
     };
     uint32_t upto = 0;
     for (int base = 0; base < a.experts; base += 64) {

@@ -94,14 +94,15 @@ __device__ __forceinline__ bf16x8_t dequant8(uint32_t w, float s) {
     return o;
 }
 
-// The same without their scale, times 8 elements of a token, added to `sum`.
+// The same without their scale, times 8 elements of a token over 128, added to `sum`:
+// 16 products of the largest elements with the largest codes stay finite.
 __device__ __forceinline__ float dot8(uint32_t w, bf16x8_t x, float sum) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const bf16x2_t v = i == 0   ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0)
-                           : i == 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1)
-                           : i == 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2)
-                                    : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3);
+        const bf16x2_t v = i == 0   ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 0x1p-7f, 0)
+                           : i == 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 0x1p-7f, 1)
+                           : i == 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 0x1p-7f, 2)
+                                    : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 0x1p-7f, 3);
         sum = __builtin_amdgcn_fdot2_f32_bf16(v, bf16x2_t{x[2 * i], x[2 * i + 1]}, sum, false);
     }
     return sum;
@@ -141,7 +142,7 @@ __device__ __forceinline__ bool find_rows(const WeightOnlyArgs& a, int64_t slot,
     for (int base = 0; base < a.experts; base += 64) {
         GroupRows r{0, 0};
         if (base + lane < a.experts) r = group_rows(a.offsets, base + lane, (int)a.rows);
-        const int n = (r.end - r.begin + per_block - 1) / per_block;
+        const int n = (int)(((uint32_t)(r.end - r.begin) + (uint32_t)(per_block - 1)) / (uint32_t)per_block);
         const int upto = wave_scan(n);
         const uint64_t votes = __ballot(before + upto > slot);
         if (votes) {
@@ -213,8 +214,8 @@ __global__ __launch_bounds__(kThreads, 4) void one_token_kernel(WeightOnlyArgs a
             }
             const float d0 = dot8(c[i].w[1], xv[1], dot8(c[i].w[0], xv[0], 0.0f));
             const float d1 = dot8(c[i].w[3], xv[3], dot8(c[i].w[2], xv[2], 0.0f));
-            sum[i] = __builtin_fmaf(d0, s0 * 0x1p112f, sum[i]);
-            sum[i] = __builtin_fmaf(d1, s1 * 0x1p112f, sum[i]);
+            sum[i] = __builtin_fmaf(d0, s0 * 0x1p119f, sum[i]);
+            sum[i] = __builtin_fmaf(d1, s1 * 0x1p119f, sum[i]);
         }
     }
 
