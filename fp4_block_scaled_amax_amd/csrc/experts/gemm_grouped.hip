@@ -201,30 +201,19 @@ struct Lds {
     static_assert(4 * kWave <= kBytes, "the epilogue has room");
 };
 
-// rows of codes begin at multiples of 8 bytes, rows of scales anywhere
-typedef u32x4 u32x4_at8 __attribute__((aligned(8)));
-typedef u32x2 u32x2_at1 __attribute__((aligned(1)));
-
-// One step of a row where K is no multiple of 128: the 16-byte unit `unit` of its
-// codes, or its 8 scale bytes.  In a step that K cuts short blocks are clamped into
-// the row, and blocks past K get the scale 0, whose factor m = 0 makes every code 0.
-__device__ __forceinline__ u32x4 load_unit(const uint8_t* row, int64_t K, int64_t k0, int unit) {
-    if (k0 + kBK <= K) return *reinterpret_cast<const u32x4_at8*>(row + k0 / 2 + 16 * unit);
-    const int64_t ka = min(k0 + 32 * unit, K - 16), kb = min(k0 + 32 * unit + 16, K - 16);
-    const u32x2 x = *reinterpret_cast<const u32x2*>(row + ka / 2);
-    const u32x2 y = *reinterpret_cast<const u32x2*>(row + kb / 2);
-    return u32x4{x.x, x.y, y.x, y.y};
-}
-__device__ __forceinline__ u32x2 load_scales(const uint8_t* row, int64_t K, int64_t k0) {
-    const int64_t b0 = k0 / 16, blocks = K / 16;
-    if (b0 + 8 <= blocks) return *reinterpret_cast<const u32x2_at1*>(row + b0);
-    uint32_t w[2] = {0u, 0u};
+// 4 scale bytes of a row, from byte b on, where K is no multiple of 128: rows of scales
+// begin anywhere.  Blocks past K get the scale 0, whose factor m = 0 makes every code
+// 0.
+typedef uint32_t u32_at1 __attribute__((aligned(1)));
+__device__ __forceinline__ uint32_t load_scales(const uint8_t* row, uint32_t blocks, uint32_t b) {
+    if (b + 4 <= blocks) return *reinterpret_cast<const u32_at1*>(row + b);
+    uint32_t w = 0u;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t v = row[min(b0 + j, blocks - 1)];
-        w[j >> 2] |= (b0 + j < blocks ? v : 0u) << (8 * (j & 3));
+    for (uint32_t j = 0; j < 4; ++j) {
+        const uint32_t v = row[min(b + j, blocks - 1)];
+        w |= (b + j < blocks ? v : 0u) << (8 * j);
     }
-    return u32x2{w[0], w[1]};
+    return w;
 }
 
 // One tile of 32 RI WM rows x 128 columns, by WM x WN waves of RI x CJ 32 x 32
@@ -232,15 +221,16 @@ __device__ __forceinline__ u32x2 load_scales(const uint8_t* row, int64_t K, int6
 //
 // A step's codes stand in LDS row by row, 64 bytes each, 16-byte unit u of row i at u
 // ^ (i / 4 % 4), so that 16 lanes read a unit of 16 rows without bank conflicts.
-// They come straight from memory, a step ahead of the one that is multiplied, where
-// K is a multiple of 128 (DIRECT); else through registers, since rows are not
-// aligned then and the last step is masked.
+// They come straight from memory, a step ahead of the one that is multiplied.  Where K
+// is no multiple of 128 (not WHOLE) the last step's come in 4 bytes a lane, each
+// clamped into its row, and scales through registers, since their rows begin anywhere
+// then: the last step's are masked.
 //
 // Lane (r, h) = (lane % 32, lane / 32) owns elements [64 h, 64 h + 64) of a row's
 // step: 2 units, 4 blocks, 8 matrix instructions.  A and B agree on it, so the sums
 // are those of the plain order.  A scale byte is expanded where it is used: 16 rows'
 // bytes mostly name few table entries.
-template <int BM, int RI, int CJ, int WM, int WN, bool DIRECT>
+template <int BM, int RI, int CJ, int WM, int WN, bool WHOLE>
 __device__ __forceinline__ void compute_tile(const Tile& t, uint8_t* smem, const GemmGroupedArgs& g) {
     using L = Lds<BM>;
     constexpr int kRowsA = 32 * RI * WM;
@@ -269,42 +259,51 @@ __device__ __forceinline__ void compute_tile(const Tile& t, uint8_t* smem, const
     osb = (uint32_t)min(scale_row, t.cols - 1) * (uint32_t)t.bs_stride;
     const uint8_t *a = t.a, *as = t.as, *b = t.b, *bs = t.bs;  // scalar: so are all of a tile's values
     const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
+    const uint32_t K = (uint32_t)t.K;
     auto stage = [&](int step, int at) __attribute__((always_inline)) {
         const uint32_t to = lds + at * L::kStage;
         const int64_t c = (int64_t)step * (kBK / 2), s = (int64_t)step * (kBK / 16);
+        if (WHOLE || (uint32_t)(step + 1) * kBK <= K) {
 #pragma unroll
-        for (int i = 0; i < kCodeTurnsA; ++i)
-            load_to_lds16(a + c, oa[i] + 16 * unit, to + L::kCodesA + 1024 * (wave + 4 * i));
+            for (int i = 0; i < kCodeTurnsA; ++i)
+                load_to_lds16(a + c, oa[i] + 16 * unit, to + L::kCodesA + 1024 * (wave + 4 * i));
 #pragma unroll
-        for (int i = 0; i < kCodeTurnsB; ++i) load_to_lds16(b + c, ob[i] + 16 * unit, to + L::kCodesB + 1024 * (wave + 4 * i));
+            for (int i = 0; i < kCodeTurnsB; ++i) load_to_lds16(b + c, ob[i] + 16 * unit, to + L::kCodesB + 1024 * (wave + 4 * i));
+        } else {  // 16 lanes a row, 4 rows a load
+            const int sub_row = lane >> 4, sub = lane & 15;
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                const int row = 16 * wave + 4 * j + sub_row;
+                const uint32_t k = min((uint32_t)step * (kBK / 2) + 16 * ((sub >> 2) ^ j) + 4 * (sub & 3), K / 2 - 4);
 #pragma unroll
-        for (int i = 0; i < kScaleTurnsA; ++i)
-            load_to_lds4(as + s, osa[i] + 4 * (lane & 1), to + L::kScalesA + 256 * (wave + 4 * i));
-        load_to_lds4(bs + s, osb + 4 * (lane & 1), to + L::kScalesB + 256 * wave);
+                for (int i = 0; i < kCodeTurnsA; ++i)
+                    load_to_lds4(a, (uint32_t)min(row + 64 * i, t.rows - 1) * (uint32_t)t.a_stride + k,
+                                 to + L::kCodesA + 1024 * (wave + 4 * i) + 256 * j);
+#pragma unroll
+                for (int i = 0; i < kCodeTurnsB; ++i)
+                    load_to_lds4(b, (uint32_t)min(row + 64 * i, t.cols - 1) * (uint32_t)t.b_stride + k,
+                                 to + L::kCodesB + 1024 * (wave + 4 * i) + 256 * j);
+            }
+        }
+        if constexpr (WHOLE) {
+#pragma unroll
+            for (int i = 0; i < kScaleTurnsA; ++i)
+                load_to_lds4(as + s, osa[i] + 4 * (lane & 1), to + L::kScalesA + 256 * (wave + 4 * i));
+            load_to_lds4(bs + s, osb + 4 * (lane & 1), to + L::kScalesB + 256 * wave);
+        }
     };
-    u32x4 ra[kCodeTurnsA], rb[kCodeTurnsB];
-    u32x2 rsa[kScaleTurnsA], rsb;
-    auto fetch = [&](int step) __attribute__((always_inline)) {
-        const int64_t k0 = (int64_t)step * kBK;
+    uint32_t rsa[kScaleTurnsA], rsb;
+    auto fetch_scales = [&](int step) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < kCodeTurnsA; ++i) ra[i] = load_unit(a + oa[i], t.K, k0, unit);
-#pragma unroll
-        for (int i = 0; i < kCodeTurnsB; ++i) rb[i] = load_unit(b + ob[i], t.K, k0, unit);
-#pragma unroll
-        for (int i = 0; i < kScaleTurnsA; ++i) rsa[i] = load_scales(as + osa[i], t.K, k0);
-        rsb = load_scales(bs + osb, t.K, k0);
+        for (int i = 0; i < kScaleTurnsA; ++i) rsa[i] = load_scales(as + osa[i], K / 16, 8 * step + 4 * (lane & 1));
+        rsb = load_scales(bs + osb, K / 16, 8 * step + 4 * (lane & 1));
     };
-    auto put_stage = [&](int at) __attribute__((always_inline)) {
+    auto put_scales = [&](int at) __attribute__((always_inline)) {
         uint8_t* to = smem + at * L::kStage;
 #pragma unroll
-        for (int i = 0; i < kCodeTurnsA; ++i)
-            *reinterpret_cast<u32x4*>(to + L::kCodesA + 1024 * (wave + 4 * i) + 16 * lane) = ra[i];
-#pragma unroll
-        for (int i = 0; i < kCodeTurnsB; ++i) *reinterpret_cast<u32x4*>(to + L::kCodesB + 1024 * (wave + 4 * i) + 16 * lane) = rb[i];
-#pragma unroll
         for (int i = 0; i < kScaleTurnsA; ++i)
-            *reinterpret_cast<uint32_t*>(to + L::kScalesA + 256 * (wave + 4 * i) + 4 * lane) = lane & 1 ? rsa[i].y : rsa[i].x;
-        *reinterpret_cast<uint32_t*>(to + L::kScalesB + 256 * wave + 4 * lane) = lane & 1 ? rsb.y : rsb.x;
+            *reinterpret_cast<uint32_t*>(to + L::kScalesA + 256 * (wave + 4 * i) + 4 * lane) = rsa[i];
+        *reinterpret_cast<uint32_t*>(to + L::kScalesB + 256 * wave + 4 * lane) = rsb;
     };
 
     const int row_a = wm * 32 * RI + r, row_b = wn * 32 * CJ + r;
@@ -318,19 +317,18 @@ __device__ __forceinline__ void compute_tile(const Tile& t, uint8_t* smem, const
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
     if (steps > 0) {
-        if constexpr (DIRECT) {
-            stage(0, 0);
-        } else {
-            fetch(0);
-            put_stage(0);
+        stage(0, 0);
+        if constexpr (!WHOLE) {
+            fetch_scales(0);
+            put_scales(0);
         }
     }
     for (int step = 0; step < steps; ++step) {
         const uint8_t* cur = smem + (step & 1) * L::kStage;
         step_ready();
         if (step + 1 < steps) {
-            if constexpr (DIRECT) stage(step + 1, (step + 1) & 1);
-            else fetch(step + 1);
+            stage(step + 1, (step + 1) & 1);
+            if constexpr (!WHOLE) fetch_scales(step + 1);
         }
         uint32_t sa[RI], sb[CJ];
 #pragma unroll
@@ -368,8 +366,8 @@ __device__ __forceinline__ void compute_tile(const Tile& t, uint8_t* smem, const
                 }
             }
         }
-        if constexpr (!DIRECT)
-            if (step + 1 < steps) put_stage((step + 1) & 1);
+        if constexpr (!WHOLE)
+            if (step + 1 < steps) put_scales((step + 1) & 1);
     }
     step_ready();  // all waves are past their last step: the stages are free
 
@@ -381,14 +379,14 @@ __device__ __forceinline__ void compute_tile(const Tile& t, uint8_t* smem, const
     if (g.amax) amax_commit(tmax, g.amax);
 }
 
-template <int BM, bool DIRECT>
+template <int BM, bool WHOLE>
 __device__ __forceinline__ void compute(const Tile& t, uint8_t* smem, const GemmGroupedArgs& g) {
     if constexpr (BM == 256) {
-        if (t.rows > 128) return compute_tile<BM, 4, 2, 2, 2, DIRECT>(t, smem, g);
+        if (t.rows > 128) return compute_tile<BM, 4, 2, 2, 2, WHOLE>(t, smem, g);
     }
-    if (t.rows > 64) compute_tile<BM, 2, 2, 2, 2, DIRECT>(t, smem, g);
-    else if (t.rows > 32) compute_tile<BM, 1, 2, 2, 2, DIRECT>(t, smem, g);
-    else compute_tile<BM, 1, 1, 1, 4, DIRECT>(t, smem, g);
+    if (t.rows > 64) compute_tile<BM, 2, 2, 2, 2, WHOLE>(t, smem, g);
+    else if (t.rows > 32) compute_tile<BM, 1, 2, 2, 2, WHOLE>(t, smem, g);
+    else compute_tile<BM, 1, 1, 1, 4, WHOLE>(t, smem, g);
 }
 
 // Consecutive workgroups go to the 8 XCDs in turn: each takes a contiguous range
@@ -463,7 +461,7 @@ __device__ __forceinline__ bool find_tile(const GemmGroupedArgs& a, uint32_t id,
     return false;
 }
 
-template <int BM, bool DIRECT>
+template <int BM, bool WHOLE>
 __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_nt_kernel(GemmGroupedArgs g) {
     using L = Lds<BM>;
     __shared__ __align__(16) uint8_t smem[L::kBytes];
@@ -490,7 +488,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_nt_kernel(GemmGroupe
     t.c = m0 * g.N + n0;
     t.sa256 = *g.a_ts * 256.0f;
     t.sb = g.b_ts[expert * g.b_ts_step];
-    compute<BM, DIRECT>(t, smem, g);
+    compute<BM, WHOLE>(t, smem, g);
 }
 
 template <int BM>
@@ -526,13 +524,13 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_wgrad_kernel(GemmGro
     compute<BM, true>(t, smem, g);
 }
 
-template <int BM, bool DIRECT>
+template <int BM, bool WHOLE>
 void launch_nt(GemmGroupedArgs g, hipStream_t stream) {
     // an expert's rows make at most rows / BM tiles and one more
     const int64_t row_tiles = g.rows / BM + (g.experts < g.rows ? g.experts : g.rows);
     in_launches(row_tiles * ((g.N + kBN - 1) / kBN), kThreads, [&](int64_t first, dim3 grid) {
         g.first = first;
-        hipLaunchKernelGGL((gemm_grouped_nt_kernel<BM, DIRECT>), grid, dim3(kThreads), 0, stream, g);
+        hipLaunchKernelGGL((gemm_grouped_nt_kernel<BM, WHOLE>), grid, dim3(kThreads), 0, stream, g);
     });
 }
 
@@ -555,10 +553,9 @@ void launch_gemm_grouped_nt(const GemmGroupedArgs& g, hipStream_t stream) {
     // rows of average experts: the tiles that 256 rows each make
     const int64_t each = (g.rows + g.experts - 1) / g.experts;
     const int64_t tiles = (g.experts < g.rows ? g.experts : g.rows) * ((each + 255) / 256) * ((g.N + kBN - 1) / kBN);
-    // through registers 256 rows spill, and steps take twice as long
-    if (g.K % kBK != 0) launch_nt<128, false>(g, stream);
-    else if (tiles >= kFew) launch_nt<256, true>(g, stream);
-    else launch_nt<128, true>(g, stream);
+    const bool whole = g.K % kBK == 0;
+    if (tiles >= kFew) whole ? launch_nt<256, true>(g, stream) : launch_nt<256, false>(g, stream);
+    else whole ? launch_nt<128, true>(g, stream) : launch_nt<128, false>(g, stream);
 }
 
 void launch_gemm_grouped_wgrad(const GemmGroupedArgs& g, hipStream_t stream) {
