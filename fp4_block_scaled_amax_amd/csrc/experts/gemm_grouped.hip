@@ -34,6 +34,7 @@ namespace {
 
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -115,7 +116,8 @@ __device__ __forceinline__ void put(uint16_t& to, float v, uint32_t& tmax) {
 // pieces of rows (bf16; 128 in fp32), and that bounds wide and short products; so
 // each 32 rows pass through this wave's part of the staging buffers, which no one
 // needs any more, and leave in 16 bytes per lane, whole rows of the wave's tile at a
-// time: 1.07 GB of bf16 stored alone FIGURE.  Where rows of C do not begin at
+// time: 16384 x 32768 results of bf16 stored alone
+// take 255 us so, and 561 us without.  Where rows of C do not begin at
 // multiples of 16 bytes they are stored directly.  Returns the largest magnitude of
 // what bf16 stores hold; rows and columns past the tile repeat its last ones, so
 // they need no exception.
@@ -389,6 +391,165 @@ __device__ __forceinline__ void compute(const Tile& t, uint8_t* smem, const Gemm
     else compute_tile<BM, 1, 1, 1, 4, WHOLE>(t, smem, g);
 }
 
+// ---- few tiles: the waves of a workgroup share out the contraction
+
+// 16 bytes of codes of a row from element k on (a multiple of 32), K being no multiple
+// of 128: blocks past K are clamped into the row.
+typedef u32x4 u32x4_at8 __attribute__((aligned(8)));
+__device__ __forceinline__ u32x4 load_codes(const uint8_t* row, uint32_t K, uint32_t k) {
+    if (k + 32 <= K) return *reinterpret_cast<const u32x4_at8*>(row + k / 2);
+    const u32x2 x = *reinterpret_cast<const u32x2*>(row + min(k, K - 16) / 2);
+    const u32x2 y = *reinterpret_cast<const u32x2*>(row + min(k + 16, K - 16) / 2);
+    return u32x4{x.x, x.y, y.x, y.y};
+}
+
+// One tile of 32 RI rows x 32 CJ columns: wave w takes steps w, w + 4, ... from memory
+// to registers, a step ahead; then the waves' sums are joined in LDS, in a fixed
+// order.
+constexpr int kSplit = 4, kSplitRows = 64, kSplitCols = 64;
+struct SplitLds {
+    static constexpr int kRow = kSplitCols + 4, kLut = 4 * kSplit * kSplitRows * kRow, kBytes = kLut + 1024;  // floats of a row
+};
+template <int RI, int CJ>
+struct Step {
+    u32x4 ca[RI][2], cb[CJ][2];
+    uint32_t sa[RI], sb[CJ];
+};
+template <int RI, int CJ, bool WHOLE>
+__device__ __forceinline__ void split_tile(const Tile& t, uint8_t* smem, const GemmGroupedArgs& g) {
+    using L = SplitLds;
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t K = (uint32_t)t.K;
+    const uint32_t* lut = reinterpret_cast<const uint32_t*>(smem + L::kLut);
+    const uint8_t *a = t.a, *as = t.as, *b = t.b, *bs = t.bs;
+    // rows past the tile repeat its last one, their results are not stored; a row's
+    // scales begin at an eighth of its codes' offset
+    uint32_t oa[RI], ob[CJ];
+#pragma unroll
+    for (int i = 0; i < RI; ++i) oa[i] = (uint32_t)min(32 * i + r, t.rows - 1) * (uint32_t)t.a_stride;
+#pragma unroll
+    for (int j = 0; j < CJ; ++j) ob[j] = (uint32_t)min(32 * j + r, t.cols - 1) * (uint32_t)t.b_stride;
+    auto load = [&](Step<RI, CJ>& s, uint32_t k) __attribute__((always_inline)) {
+        const uint32_t c = k / 2 + 32 * h;
+        if (WHOLE || k + kBK <= K) {
+#pragma unroll
+            for (int i = 0; i < RI; ++i) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) s.ca[i][p] = *reinterpret_cast<const u32x4_at8*>(a + (oa[i] + c + 16 * p));
+                s.sa[i] = *reinterpret_cast<const u32_at1*>(as + ((oa[i] + c) >> 3));
+            }
+#pragma unroll
+            for (int j = 0; j < CJ; ++j) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) s.cb[j][p] = *reinterpret_cast<const u32x4_at8*>(b + (ob[j] + c + 16 * p));
+                s.sb[j] = *reinterpret_cast<const u32_at1*>(bs + ((ob[j] + c) >> 3));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < RI; ++i) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) s.ca[i][p] = load_codes(a + oa[i], K, k + 64 * h + 32 * p);
+                s.sa[i] = load_scales(as + (oa[i] >> 3), K / 16, k / 16 + 4 * h);
+            }
+#pragma unroll
+            for (int j = 0; j < CJ; ++j) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) s.cb[j][p] = load_codes(b + ob[j], K, k + 64 * h + 32 * p);
+                s.sb[j] = load_scales(bs + (ob[j] >> 3), K / 16, k / 16 + 4 * h);
+            }
+        }
+    };
+    f32x16_t acc[RI][CJ];
+#pragma unroll
+    for (int i = 0; i < RI; ++i)
+#pragma unroll
+        for (int j = 0; j < CJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+    Step<RI, CJ> next;
+    if (wave * kBK < K) load(next, wave * kBK);
+    __syncthreads();  // the table of scales is there
+    for (uint32_t k = wave * kBK; k < K; k += kSplit * kBK) {
+        const Step<RI, CJ> cur = next;
+        if (k + kSplit * kBK < K) load(next, k + kSplit * kBK);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+#pragma unroll
+            for (int block = 0; block < 2; ++block) {
+                uint32_t ea[RI], eb[CJ];
+#pragma unroll
+                for (int i = 0; i < RI; ++i) ea[i] = lut[(cur.sa[i] >> (8 * (2 * p + block))) & 0xFFu];
+#pragma unroll
+                for (int j = 0; j < CJ; ++j) eb[j] = lut[(cur.sb[j] >> (8 * (2 * p + block))) & 0xFFu];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    f16x8_t fa[RI], fb[CJ];
+#pragma unroll
+                    for (int i = 0; i < RI; ++i) fa[i] = dequant8(cur.ca[i][p][2 * block + s], ea[i]);
+#pragma unroll
+                    for (int j = 0; j < CJ; ++j) fb[j] = dequant8(cur.cb[j][p][2 * block + s], eb[j]);
+#pragma unroll
+                    for (int i = 0; i < RI; ++i)
+#pragma unroll
+                        for (int j = 0; j < CJ; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+                }
+            }
+        }
+    }
+
+    // ---- the waves' sums: accumulator e of lane (r, h) is row 8 (e / 4) + 4 h + e % 4,
+    // column r of its 32 x 32 tile
+    float* sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int i = 0; i < RI; ++i)
+#pragma unroll
+        for (int j = 0; j < CJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                sums[(wave * 32 * RI + 32 * i + 8 * (e >> 2) + 4 * h + (e & 3)) * L::kRow + 32 * j + r] = acc[i][j][e];
+    __syncthreads();
+    // 4 columns per thread; columns come in fours where rows of C are aligned
+    constexpr int kLanes = 32 * CJ / 4;
+    uint32_t tmax = 0u;
+#pragma unroll
+    for (int m = 0; m < 32 * RI * kLanes / kThreads; ++m) {
+        const int row = (m * kThreads + (int)threadIdx.x) / kLanes, col = 4 * (threadIdx.x % kLanes);
+        f32x4_t v = *reinterpret_cast<const f32x4_t*>(sums + row * L::kRow + col);
+#pragma unroll
+        for (int w = 1; w < kSplit; ++w) v += *reinterpret_cast<const f32x4_t*>(sums + (w * 32 * RI + row) * L::kRow + col);
+        if (row >= t.rows) continue;
+        const int64_t to = t.c + row * g.N + col;
+        if (g.c_bf16) {
+            uint16_t o[4];
+#pragma unroll
+            for (int d = 0; d < 4; ++d) put(o[d], (v[d] * t.sa256) * t.sb, tmax);
+            uint16_t* C = (uint16_t*)g.c + to;
+            if (g.N % 4 == 0) {
+                if (col < t.cols) *reinterpret_cast<uint64_t*>(C) = (uint64_t)o[3] << 48 | (uint64_t)o[2] << 32 | (uint32_t)o[1] << 16 | o[0];
+            } else {
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    if (col + d < t.cols) C[d] = o[d];
+            }
+        } else {
+#pragma unroll
+            for (int d = 0; d < 4; ++d) v[d] = (v[d] * t.sa256) * t.sb;
+            float* C = (float*)g.c + to;
+            if (g.N % 4 == 0) {
+                if (col < t.cols) *reinterpret_cast<f32x4_t*>(C) = v;
+            } else {
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    if (col + d < t.cols) C[d] = v[d];
+            }
+        }
+    }
+    if (g.amax) amax_commit(tmax, g.amax);
+}
+
 // Consecutive workgroups go to the 8 XCDs in turn: each takes a contiguous range
 // of the n tiles, so that an L2 holds what its workgroups share.
 template <typename T>
@@ -461,21 +622,18 @@ __device__ __forceinline__ bool find_tile(const GemmGroupedArgs& a, uint32_t id,
     return false;
 }
 
-template <int BM, bool WHOLE>
-__global__ __launch_bounds__(kThreads, 2) void gemm_grouped_nt_kernel(GemmGroupedArgs g) {
-    using L = Lds<BM>;
-    __shared__ __align__(16) uint8_t smem[L::kBytes];
+// The tile of a workgroup of fprop and dgrad in tiles of up to BM x BN.
+template <int BM, int BN>
+__device__ __forceinline__ bool nt_tile(const GemmGroupedArgs& g, Tile& t) {
     Found f;
-    const uint32_t tiles_n = (uint32_t)((g.N + kBN - 1) / kBN);
-    if (!find_tile<BM>(g, (uint32_t)g.first + blockIdx.x, tiles_n, f)) return;
-    reinterpret_cast<uint32_t*>(smem + L::kLut)[threadIdx.x] = expand_scale(threadIdx.x);
+    const uint32_t tiles_n = (uint32_t)((g.N + BN - 1) / BN);
+    if (!find_tile<BM>(g, (uint32_t)g.first + blockIdx.x, tiles_n, f)) return false;
     const int expert = __builtin_amdgcn_readfirstlane(f.g);
     const int begin = __builtin_amdgcn_readfirstlane(f.begin), end = __builtin_amdgcn_readfirstlane(f.end);
     const int full = full_tiles<BM>(end - begin);
     uint32_t tm = full, tn = __builtin_amdgcn_readfirstlane(f.tile);
     if (__builtin_amdgcn_readfirstlane(f.full)) tile_of(tn, full, tiles_n, tm, tn);
-    const int64_t m0 = begin + (int64_t)tm * BM, n0 = (int64_t)tn * kBN;
-    Tile t;
+    const int64_t m0 = begin + (int64_t)tm * BM, n0 = (int64_t)tn * BN;
     t.a_stride = t.b_stride = g.K / 2;
     t.as_stride = t.bs_stride = g.K / 16;
     t.K = g.K;
@@ -484,19 +642,17 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_nt_kernel(GemmGroupe
     t.b = g.b_codes + (expert * g.N + n0) * t.b_stride;
     t.bs = g.b_scales + (expert * g.N + n0) * t.bs_stride;
     t.rows = (int)min(end - m0, (int64_t)BM);
-    t.cols = (int)min(g.N - n0, (int64_t)kBN);
+    t.cols = (int)min(g.N - n0, (int64_t)BN);
     t.c = m0 * g.N + n0;
     t.sa256 = *g.a_ts * 256.0f;
     t.sb = g.b_ts[expert * g.b_ts_step];
-    compute<BM, WHOLE>(t, smem, g);
+    return true;
 }
 
-template <int BM>
-__global__ __launch_bounds__(kThreads, 2) void gemm_grouped_wgrad_kernel(GemmGroupedArgs g) {
-    using L = Lds<BM>;
-    __shared__ __align__(16) uint8_t smem[L::kBytes];
-    reinterpret_cast<uint32_t*>(smem + L::kLut)[threadIdx.x] = expand_scale(threadIdx.x);
-    const uint32_t tiles_m = (uint32_t)((g.M + BM - 1) / BM), tiles_n = (uint32_t)((g.N + kBN - 1) / kBN);
+// The tile of a workgroup of wgrad.
+template <int BM, int BN>
+__device__ __forceinline__ void wgrad_tile(const GemmGroupedArgs& g, Tile& t) {
+    const uint32_t tiles_m = (uint32_t)((g.M + BM - 1) / BM), tiles_n = (uint32_t)((g.N + BN - 1) / BN);
     const int64_t j = xcd_order(g.first + blockIdx.x, (int64_t)g.experts * tiles_m * tiles_n);
     const int expert = __builtin_amdgcn_readfirstlane((int)(j / (tiles_m * tiles_n)));
     uint32_t tm, tn;
@@ -507,8 +663,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_wgrad_kernel(GemmGro
     own.begin = __builtin_amdgcn_readfirstlane(own.begin);
     own.end = __builtin_amdgcn_readfirstlane(own.end);
     const int64_t padded = 128 * ((g.rows + 127) / 128 + g.experts), p = padded_begin(own.begin, expert);
-    const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * kBN;
-    Tile t;
+    const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
     t.a_stride = t.b_stride = padded / 2;
     t.as_stride = t.bs_stride = padded / 16;
     t.K = ((int64_t)own.end - own.begin + 127) / 128 * 128;
@@ -517,50 +672,103 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_wgrad_kernel(GemmGro
     t.b = g.b_codes + n0 * t.b_stride + p / 2;
     t.bs = g.b_scales + n0 * t.bs_stride + p / 16;
     t.rows = (int)min(g.M - m0, (int64_t)BM);
-    t.cols = (int)min(g.N - n0, (int64_t)kBN);
+    t.cols = (int)min(g.N - n0, (int64_t)BN);
     t.c = (expert * g.M + m0) * g.N + n0;
     t.sa256 = *g.a_ts * 256.0f;
     t.sb = *g.b_ts;
-    compute<BM, true>(t, smem, g);
 }
 
 template <int BM, bool WHOLE>
-void launch_nt(GemmGroupedArgs g, hipStream_t stream) {
-    // an expert's rows make at most rows / BM tiles and one more
-    const int64_t row_tiles = g.rows / BM + (g.experts < g.rows ? g.experts : g.rows);
-    in_launches(row_tiles * ((g.N + kBN - 1) / kBN), kThreads, [&](int64_t first, dim3 grid) {
-        g.first = first;
-        hipLaunchKernelGGL((gemm_grouped_nt_kernel<BM, WHOLE>), grid, dim3(kThreads), 0, stream, g);
-    });
+__global__ __launch_bounds__(kThreads, 2) void gemm_grouped_nt_kernel(GemmGroupedArgs g) {
+    using L = Lds<BM>;
+    __shared__ __align__(16) uint8_t smem[L::kBytes];
+    Tile t;
+    if (!nt_tile<BM, kBN>(g, t)) return;
+    reinterpret_cast<uint32_t*>(smem + L::kLut)[threadIdx.x] = expand_scale(threadIdx.x);
+    compute<BM, WHOLE>(t, smem, g);
 }
 
 template <int BM>
-void launch_wgrad(GemmGroupedArgs g, hipStream_t stream) {
-    const int64_t tiles = g.experts * ((g.M + BM - 1) / BM) * ((g.N + kBN - 1) / kBN);
-    in_launches(tiles, kThreads, [&](int64_t first, dim3 grid) {
+__global__ __launch_bounds__(kThreads, 2) void gemm_grouped_wgrad_kernel(GemmGroupedArgs g) {
+    using L = Lds<BM>;
+    __shared__ __align__(16) uint8_t smem[L::kBytes];
+    reinterpret_cast<uint32_t*>(smem + L::kLut)[threadIdx.x] = expand_scale(threadIdx.x);
+    Tile t;
+    wgrad_tile<BM, kBN>(g, t);
+    compute<BM, true>(t, smem, g);
+}
+
+template <bool WHOLE>
+__device__ __forceinline__ void split(const Tile& t, uint8_t* smem, const GemmGroupedArgs& g) {
+    reinterpret_cast<uint32_t*>(smem + SplitLds::kLut)[threadIdx.x] = expand_scale(threadIdx.x);
+    if (t.rows > 32) split_tile<2, 2, WHOLE>(t, smem, g);
+    else split_tile<1, 2, WHOLE>(t, smem, g);
+}
+
+template <bool WHOLE>
+__global__ __launch_bounds__(kThreads, 2) void gemm_grouped_nt_split_kernel(GemmGroupedArgs g) {
+    __shared__ __align__(16) uint8_t smem[SplitLds::kBytes];
+    Tile t;
+    if (nt_tile<kSplitRows, kSplitCols>(g, t)) split<WHOLE>(t, smem, g);
+}
+
+__global__ __launch_bounds__(kThreads, 2) void gemm_grouped_wgrad_split_kernel(GemmGroupedArgs g) {
+    __shared__ __align__(16) uint8_t smem[SplitLds::kBytes];
+    Tile t;
+    wgrad_tile<kSplitRows, kSplitCols>(g, t);
+    split<true>(t, smem, g);
+}
+
+template <int BM, int BN, typename KERNEL>
+void launch_nt(GemmGroupedArgs g, hipStream_t stream, KERNEL kernel) {
+    // an expert's rows make at most rows / BM tiles and one more
+    const int64_t row_tiles = g.rows / BM + (g.experts < g.rows ? g.experts : g.rows);
+    in_launches(row_tiles * ((g.N + BN - 1) / BN), kThreads, [&](int64_t first, dim3 grid) {
         g.first = first;
-        hipLaunchKernelGGL(gemm_grouped_wgrad_kernel<BM>, grid, dim3(kThreads), 0, stream, g);
+        hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, g);
     });
 }
 
-// 256 rows where that leaves work for two workgroups on each of the 256 CUs, else 128
-// (FIGURE).
+template <int BM, int BN, typename KERNEL>
+void launch_wgrad(GemmGroupedArgs g, hipStream_t stream, KERNEL kernel) {
+    const int64_t tiles = g.experts * ((g.M + BM - 1) / BM) * ((g.N + BN - 1) / BN);
+    in_launches(tiles, kThreads, [&](int64_t first, dim3 grid) {
+        g.first = first;
+        hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, g);
+    });
+}
+
+// Two workgroups on each of the 256 CUs.
 constexpr int64_t kFew = 512;
+
+// Tiles of 64 x 64 with split contractions while all of them run at once: 4 experts of
+// 128 rows, 4096 -> 2048 (256 of them), 38 -> 19 us, 4096 -> 4096 (512) 41 -> 32 us;
+// 16 experts of 64 rows, 4096 -> 4096 (1024), would lose, 50 -> 57 us.  Tiles of 256
+// rows where those are enough for all CUs: 8 experts of 1024 rows, 4096 -> 4096
+// (1024), 264 -> 232 us; 8 of 512 rows, 4096 -> 2048 (256), would lose, 73 -> 78 us.
+template <bool WHOLE>
+void dispatch_nt(const GemmGroupedArgs& g, hipStream_t stream) {
+    // tiles that experts with the mean number of rows make
+    const int64_t some = g.experts < g.rows ? g.experts : g.rows, each = (g.rows + some - 1) / some;
+    auto tiles = [&](int rows, int cols) { return some * ((each + rows - 1) / rows) * ((g.N + cols - 1) / cols); };
+    if (tiles(kSplitRows, kSplitCols) <= kFew) launch_nt<kSplitRows, kSplitCols>(g, stream, gemm_grouped_nt_split_kernel<WHOLE>);
+    else if (tiles(256, kBN) < kFew) launch_nt<128, kBN>(g, stream, gemm_grouped_nt_kernel<128, WHOLE>);
+    else launch_nt<256, kBN>(g, stream, gemm_grouped_nt_kernel<256, WHOLE>);
+}
 
 }  // namespace
 
 void launch_gemm_grouped_nt(const GemmGroupedArgs& g, hipStream_t stream) {
-    // rows of average experts: the tiles that 256 rows each make
-    const int64_t each = (g.rows + g.experts - 1) / g.experts;
-    const int64_t tiles = (g.experts < g.rows ? g.experts : g.rows) * ((each + 255) / 256) * ((g.N + kBN - 1) / kBN);
-    const bool whole = g.K % kBK == 0;
-    if (tiles >= kFew) whole ? launch_nt<256, true>(g, stream) : launch_nt<256, false>(g, stream);
-    else whole ? launch_nt<128, true>(g, stream) : launch_nt<128, false>(g, stream);
+    g.K % kBK == 0 ? dispatch_nt<true>(g, stream) : dispatch_nt<false>(g, stream);
 }
 
+// The same rule: one expert of 2048 rows, 1024 x 1024, 22 -> 11 us split; 4 experts of
+// 512 rows, 1024 x 1024 (1024 tiles), would lose, 12 -> 16 us.
 void launch_gemm_grouped_wgrad(const GemmGroupedArgs& g, hipStream_t stream) {
-    if (g.experts * ((g.M + 255) / 256) * ((g.N + kBN - 1) / kBN) >= kFew) launch_wgrad<256>(g, stream);
-    else launch_wgrad<128>(g, stream);
+    auto tiles = [&](int rows, int cols) { return g.experts * ((g.M + rows - 1) / rows) * ((g.N + cols - 1) / cols); };
+    if (tiles(kSplitRows, kSplitCols) <= kFew) launch_wgrad<kSplitRows, kSplitCols>(g, stream, gemm_grouped_wgrad_split_kernel);
+    else if (tiles(256, kBN) < kFew) launch_wgrad<128, kBN>(g, stream, gemm_grouped_wgrad_kernel<128>);
+    else launch_wgrad<256, kBN>(g, stream, gemm_grouped_wgrad_kernel<256>);
 }
 
 }  // namespace ue5m3fp4

@@ -83,12 +83,14 @@ def check(out, a, b, bf16):
 
 # --------------------------------------------------------------- tall tiles --
 
-# behind full tiles of 256 rows: rests of 1 .. 32, 33 .. 64, 65 .. 128 and 129 .. 255, and none
+# Tiles of 256 rows (N 8200), of 128 (N 700) and of 64 with split contractions (N 100).
+# Behind full tiles: rests of 1 .. 32, 33 .. 64, 65 .. 128 and 129 .. 255, and none
 TALL = [256, 1, 33, 65, 129, 257, 300, 384, 385, 0, 511, 512]
 
 
 @pytest.mark.parametrize("bf16", [False, True])
-@pytest.mark.parametrize("N,K", [(8200, 128), (8197, 384), (8200, 272)])
+@pytest.mark.parametrize("N,K", [(8200, 128), (8197, 384), (8200, 272), (704, 128), (701, 1040), (720, 400), (704, 16), (704, 48),
+                                 (100, 1024), (101, 1104), (130, 528), (64, 32)])
 def test_grouped_rows_in_many_tiles(cuda_device, N, K, bf16):
     counts, before, behind = TALL, 3, 5
     off, E = offsets_of(counts, before), len(counts)
@@ -105,9 +107,9 @@ def test_grouped_rows_in_many_tiles(cuda_device, N, K, bf16):
 
 
 @pytest.mark.parametrize("bf16", [False, True])
-@pytest.mark.parametrize("M,N", [(2100, 1500), (2050, 1504), (1801, 2001)])
+@pytest.mark.parametrize("M,N", [(2100, 1500), (2050, 1504), (1801, 2001), (700, 701), (720, 704), (130, 68), (33, 67)])
 def test_wgrad_in_many_tiles(cuda_device, M, N, bf16):
-    counts = [0, 1, 300, 128, 65]
+    counts = [0, 1, 300, 128, 1165]
     off, E = offsets_of(counts, 2), len(counts)
     rows = int(off[-1]) + 1
     P = lib.rows_padded(rows, E)
