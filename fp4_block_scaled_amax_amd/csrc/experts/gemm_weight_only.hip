@@ -5,10 +5,10 @@
 // Every weight byte is read once per block of tokens, so what counts is to keep
 // loads of them in flight and to convert them fast enough.  A workgroup owns 16 RT
 // rows of W (columns of the result) and the tokens of one expert, up to a limit;
-// its 8 waves share out K and join their sums in LDS, in a fixed order.  Lane (r, q)
-// = (lane % 16, lane / 16) has 32 consecutive codes and 2 scale bytes of row r of
-// each tile of W and step of 128, and the same 32 elements of token r, so the K
-// order of the two operands of v_mfma_f32_16x16x32_bf16 agrees.
+// its waves share out K and join their sums in LDS, in a fixed order.  One token goes
+// through dot products, more through v_mfma_f32_16x16x32_bf16, for which lane (r, q)
+// = (lane % 16, lane / 16) has the same consecutive elements of row r of W and of token
+// r, so the K order of the two operands agrees.
 //
 // q s has at most 6 significant bits and lies within [2^-18, 688128], so it is
 // exact in bf16, and so are the products in fp32.
@@ -30,8 +30,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_at8 __attribute__((aligned(8)));
 typedef u32x2 u32x2_at1 __attribute__((aligned(1)));
 typedef uint16_t u16_at1 __attribute__((aligned(1)));
-
-constexpr int kWaves = 8, kThreads = 64 * kWaves;
 
 // 32 consecutive codes of a row and their 2 scale bytes.  In a step that K cuts
 // short (`whole` false) each block of 16 is clamped into the row, and blocks past K
@@ -162,11 +160,13 @@ __device__ __forceinline__ bool find_rows(const WeightOnlyArgs& a, int64_t slot,
 // elements of the token, which it keeps in registers for all rows.  The 8 waves
 // share out the chunks.  Products in v_dot2_f32_bf16, which with the conversion to
 // bf16 costs one instruction per weight, where the matrix instruction would need
-// the scale in its operand, another one; the scale enters once per block.
-template <int ROWS, bool WHOLE>
-__global__ __launch_bounds__(kThreads, 4) void one_token_kernel(WeightOnlyArgs a, Place place) {
+// the scale in its operand, another one; the scale enters once per block.  4096 ->
+// 16384 (37.7 MB) takes 8.7 us, an empty launch 2.4 us, and a kernel that only reads
+// those bytes in the same pattern 6.7 us: bound by the loads' latency and bandwidth.
+template <int ROWS, int WAVES, bool WHOLE>
+__global__ __launch_bounds__(64 * WAVES, 4) void one_token_kernel(WeightOnlyArgs a, Place place) {
     constexpr int kLoads = ROWS / 4;  // 4 rows of W per load
-    __shared__ float sums[kWaves][ROWS];
+    __shared__ float sums[WAVES][ROWS];
     const uint32_t u0 = place.tile + blockIdx.x, down = u0 / place.tiles;
     const int64_t slot = place.slot + down, n0 = (int64_t)(u0 - down * place.tiles) * ROWS;
     int g, begin, end;
@@ -197,14 +197,14 @@ __global__ __launch_bounds__(kThreads, 4) void one_token_kernel(WeightOnlyArgs a
             load_codes(next[i], codes, scales, (uint32_t)min(4 * i + q, rows - 1), K, k, whole);
     };
     if (wave * 512 < K) load(wave * 512);
-    for (uint32_t k0 = wave * 512; k0 < K; k0 += kWaves * 512) {
+    for (uint32_t k0 = wave * 512; k0 < K; k0 += WAVES * 512) {
         bf16x8_t xv[4];
         Codes c[kLoads];
 #pragma unroll
         for (int u = 0; u < 4; ++u) xv[u] = xnext[u];
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) c[i] = next[i];
-        if (k0 + kWaves * 512 < K) load(k0 + kWaves * 512);
+        if (k0 + WAVES * 512 < K) load(k0 + WAVES * 512);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             float s0 = scale_value(c[i].s, 0), s1 = scale_value(c[i].s, 1);
@@ -232,7 +232,7 @@ __global__ __launch_bounds__(kThreads, 4) void one_token_kernel(WeightOnlyArgs a
     if ((int)threadIdx.x < rows) {
         float v = sums[0][threadIdx.x];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) v += sums[w][threadIdx.x];
+        for (int w = 1; w < WAVES; ++w) v += sums[w][threadIdx.x];
         const int64_t at = begin * a.ldo + n0 + threadIdx.x;
         if (a.out_bf16) ((uint16_t*)a.out)[at] = to_bf16(v * ts);
         else ((float*)a.out)[at] = v * ts;
@@ -259,7 +259,10 @@ __device__ __forceinline__ void lds_reads_done() { asm volatile("s_waitcnt lgkmc
 // 16, lane / 16) has 32 consecutive codes of row r and the same 32 elements of token
 // r.  A wave brings its own step's tokens to LDS, in whole lines, while it multiplies
 // the step before; unit u (16 bytes) of token t stands at u ^ (t % 16) of the
-// token's 256 bytes, so that 16 tokens read a unit without bank conflicts.
+// token's 256 bytes, so that 16 tokens read a unit without bank conflicts.  64 tokens,
+// 4096 -> 16384: 25.6 us, where loads straight to registers took 74 us; bound by the
+// conversions (2 instructions a weight) and by the tokens' reads, which every
+// workgroup repeats.
 template <int RT, int TOKENS, int WAVES, bool WHOLE>
 __global__ __launch_bounds__(64 * WAVES, TOKENS > 32 ? 2 : 4) void tokens_kernel(WeightOnlyArgs a, Place place) {
     constexpr int kStep = 128, kUnits = 16;  // elements of K, and units of a token, per step
@@ -429,12 +432,13 @@ __device__ __forceinline__ u32x2 dealt(u32x2 s, uint32_t pick) {
 // The same in chunks of 4 steps: fewer loads of scales, and all of a chunk's codes
 // are on their way at once.  The tokens of PART steps stand in LDS; they are read
 // into registers before the next ones are asked for, or (4 tokens) have two places.
-template <int RT, int TOKENS, bool WHOLE>
-__global__ __launch_bounds__(kThreads, RT > 2 ? 2 : RT * TOKENS >= 32 ? 3 : 4) void chunks_kernel(WeightOnlyArgs a, Place place) {
+// 16 tokens, 16384 -> 4096: 16.4 us (2.3 TB/s), in steps of 128 it took 32 us.
+template <int RT, int TOKENS, int WAVES, bool WHOLE>
+__global__ __launch_bounds__(64 * WAVES, RT > 2 ? 2 : RT * TOKENS >= 32 ? 3 : 4) void chunks_kernel(WeightOnlyArgs a, Place place) {
     constexpr int kChunk = 512, PART = TOKENS > 4 ? 2 : 4, kPlaces = TOKENS > 4 ? 1 : 2;
     static_assert(TOKENS <= 16, "one tile of tokens");
     constexpr int kStepBytes = TOKENS * 256, kWaveBytes = kPlaces * PART * kStepBytes;
-    constexpr int kTokenBytes = kWaves * kWaveBytes, kSumBytes = kWaves * RT * 64 * 16;
+    constexpr int kTokenBytes = WAVES * kWaveBytes, kSumBytes = WAVES * RT * 64 * 16;
     __shared__ __align__(16) uint8_t smem[kTokenBytes > kSumBytes ? kTokenBytes : kSumBytes];
     const uint32_t u0 = place.tile + blockIdx.x, down = u0 / place.tiles;
     const int64_t slot = place.slot + down, n0 = (int64_t)(u0 - down * place.tiles) * (16 * RT);
@@ -475,7 +479,7 @@ __global__ __launch_bounds__(kThreads, RT > 2 ? 2 : RT * TOKENS >= 32 ? 3 : 4) v
             }
     };
     // chunk j of this wave is chunk wave + 8 j of K
-    const uint32_t first = wave * kChunk, stride = kWaves * kChunk;
+    const uint32_t first = wave * kChunk, stride = WAVES * kChunk;
     ChunkCodes w[RT];
     if (first < K) {
         load_tokens(first, xs_at);
@@ -553,12 +557,12 @@ __global__ __launch_bounds__(kThreads, RT > 2 ? 2 : RT * TOKENS >= 32 ? 3 : 4) v
 #pragma unroll
     for (int i = 0; i < RT; ++i) sums[(wave * RT + i) * 64 + lane] = acc[i];
     __syncthreads();
-    for (int e = threadIdx.x; e < RT * 64; e += kThreads) {
+    for (int e = threadIdx.x; e < RT * 64; e += 64 * WAVES) {
         const int l = e & 63, i = e / 64;
         if ((l & 15) >= tokens) continue;
         f32x4_t v = sums[e];
 #pragma unroll
-        for (int o = 1; o < kWaves; ++o) v += sums[o * (RT * 64) + e];
+        for (int o = 1; o < WAVES; ++o) v += sums[o * (RT * 64) + e];
         const int64_t to = (int64_t)begin + (l & 15), col = n0 + 16 * i + 4 * (l >> 4);
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
@@ -570,25 +574,25 @@ __global__ __launch_bounds__(kThreads, RT > 2 ? 2 : RT * TOKENS >= 32 ? 3 : 4) v
     }
 }
 
-template <int ROWS>
+template <int ROWS, int WAVES>
 void launch_one(const WeightOnlyArgs& a, hipStream_t stream) {
     const int64_t tiles_n = (a.N + ROWS - 1) / ROWS;
-    in_launches(a.rows * tiles_n, kThreads, [&](int64_t first, dim3 grid) {
+    in_launches(a.rows * tiles_n, 64 * WAVES, [&](int64_t first, dim3 grid) {
         const Place at{first / tiles_n, (uint32_t)(first % tiles_n), (uint32_t)tiles_n};
-        if (a.K % 512 == 0) hipLaunchKernelGGL((one_token_kernel<ROWS, true>), grid, dim3(kThreads), 0, stream, a, at);
-        else hipLaunchKernelGGL((one_token_kernel<ROWS, false>), grid, dim3(kThreads), 0, stream, a, at);
+        if (a.K % 512 == 0) hipLaunchKernelGGL((one_token_kernel<ROWS, WAVES, true>), grid, dim3(64 * WAVES), 0, stream, a, at);
+        else hipLaunchKernelGGL((one_token_kernel<ROWS, WAVES, false>), grid, dim3(64 * WAVES), 0, stream, a, at);
     });
 }
 
-template <int RT, int TOKENS>
+template <int RT, int TOKENS, int WAVES>
 void launch_chunks(const WeightOnlyArgs& a, hipStream_t stream) {
     const int64_t tiles_n = (a.N + 16 * RT - 1) / (16 * RT);
     int64_t slots = (a.rows + TOKENS - 1) / TOKENS;
     if (a.offsets) slots = a.rows / TOKENS + (a.experts < a.rows ? a.experts : a.rows);
-    in_launches(slots * tiles_n, kThreads, [&](int64_t first, dim3 grid) {
+    in_launches(slots * tiles_n, 64 * WAVES, [&](int64_t first, dim3 grid) {
         const Place at{first / tiles_n, (uint32_t)(first % tiles_n), (uint32_t)tiles_n};
-        if (a.K % 512 == 0) hipLaunchKernelGGL((chunks_kernel<RT, TOKENS, true>), grid, dim3(kThreads), 0, stream, a, at);
-        else hipLaunchKernelGGL((chunks_kernel<RT, TOKENS, false>), grid, dim3(kThreads), 0, stream, a, at);
+        if (a.K % 512 == 0) hipLaunchKernelGGL((chunks_kernel<RT, TOKENS, WAVES, true>), grid, dim3(64 * WAVES), 0, stream, a, at);
+        else hipLaunchKernelGGL((chunks_kernel<RT, TOKENS, WAVES, false>), grid, dim3(64 * WAVES), 0, stream, a, at);
     });
 }
 
@@ -606,6 +610,12 @@ void launch(const WeightOnlyArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// Waves that share out K, 8 or fewer: with less than a step (128 of K for up to 64
+// tokens, 512 else) or two for each wave the others idle, and workgroups of fewer waves,
+// where there are many, keep more loads in flight.  64 experts, 1024 -> 4096: 16 tokens
+// 21 -> 11 us with 2 waves, 64 tokens 56 -> 24 us with 2, 35 us with 4; 4096 -> 2048,
+// 64 tokens 50 -> 42 us with 4; one token 4096 -> 16384 9.9 -> 8.7 us with 4.  With few
+// workgroups the sum over K counts: 16384 -> 4096, 4 tokens, 12.7 us, with 4 waves 16.5.
 void launch_gemm_weight_only(const WeightOnlyArgs& a, hipStream_t stream) {
     // Tokens that a workgroup should be ready for: all, or of an expert twice the
     // mean (more than that take the weights a second time).
@@ -615,20 +625,30 @@ void launch_gemm_weight_only(const WeightOnlyArgs& a, hipStream_t stream) {
     const int64_t blocks = a.offsets ? (a.experts < a.rows ? a.experts : a.rows) : (a.rows + 63) / 64;
     const int64_t groups = (a.N + 15) / 16 * blocks;
     if (each == 1) {
-        launch_one<16>(a, stream);
+        if (groups >= 1024 && a.K <= 5120) launch_one<16, 4>(a, stream);
+        else launch_one<16, 8>(a, stream);
     } else if (each <= 4) {
-        if (groups >= 1024) launch_chunks<2, 4>(a, stream);
-        else launch_chunks<1, 4>(a, stream);
+        if (groups < 1024) launch_chunks<1, 4, 8>(a, stream);
+        else if (a.K <= 1024) launch_chunks<2, 4, 2>(a, stream);
+        else if (a.K <= 2560) launch_chunks<2, 4, 4>(a, stream);
+        else launch_chunks<2, 4, 8>(a, stream);
     } else if (each <= 16) {
-        if (groups >= 1024) launch_chunks<4, 16>(a, stream);
-        else if (groups >= 512) launch_chunks<2, 16>(a, stream);
-        else launch_chunks<1, 16>(a, stream);
+        if (groups < 512) launch_chunks<1, 16, 8>(a, stream);
+        else if (groups < 1024) launch_chunks<2, 16, 8>(a, stream);
+        else if (a.K <= 1024) launch_chunks<4, 16, 2>(a, stream);
+        else if (a.K <= 2560) launch_chunks<4, 16, 4>(a, stream);
+        else launch_chunks<4, 16, 8>(a, stream);
     } else if (each <= 32) {
-        if (groups >= 1024) launch<2, 32, 8>(a, stream);
-        else launch<1, 32, 8>(a, stream);
+        if (groups < 512 || (groups < 1024 && a.K > 5120)) launch<1, 32, 8>(a, stream);
+        else if (groups < 1024) launch<1, 32, 4>(a, stream);
+        else if (a.K <= 1024 && groups >= 4096) launch<2, 32, 2>(a, stream);
+        else if (a.K <= 5120) launch<2, 32, 4>(a, stream);
+        else launch<2, 32, 8>(a, stream);
     } else {
-        if (groups >= 512) launch<2, 64, 8>(a, stream);
-        else launch<1, 64, 8>(a, stream);
+        if (groups < 512) launch<1, 64, 8>(a, stream);
+        else if (a.K <= 1024 && groups >= 4096) launch<2, 64, 2>(a, stream);
+        else if (a.K <= 5120) launch<2, 64, 4>(a, stream);
+        else launch<2, 64, 8>(a, stream);
     }
 }
 
