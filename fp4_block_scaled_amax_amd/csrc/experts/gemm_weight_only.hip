@@ -610,45 +610,44 @@ void launch(const WeightOnlyArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// Waves that share out K, 8 or fewer: with less than a step (128 of K for up to 64
-// tokens, 512 else) or two for each wave the others idle, and workgroups of fewer waves,
-// where there are many, keep more loads in flight.  64 experts, 1024 -> 4096: 16 tokens
-// 21 -> 11 us with 2 waves, 64 tokens 56 -> 24 us with 2, 35 us with 4; 4096 -> 2048,
-// 64 tokens 50 -> 42 us with 4; one token 4096 -> 16384 9.9 -> 8.7 us with 4.  With few
-// workgroups the sum over K counts: 16384 -> 4096, 4 tokens, 12.7 us, with 4 waves 16.5.
+// What a workgroup has.  Rows of W: joining 32 or 64 halves the reads of the tokens, and
+// workgroups.  Waves, which share out K: 8 have the most loads in flight where there are
+// few workgroups (16384 -> 4096, 4 tokens, 12.7 us, with 4 waves 16.5); where there are
+// many, fewer leave none idle when K is short and join fewer sums.  Measured, us:
+//   16 tokens  1024 -> 16384        16 rows, 8 waves  8.6   32 rows, 4 waves  6.8
+//              9 experts 2064 -> 1305   32, 8        12.8       16, 4         9.0
+//              64 experts 4096 -> 2048  64, 8        92.6       32, 4        68.0
+//              64 experts 1024 -> 4096  16, 8       131         64, 2        43.9 (32, 4: 50.4)
+//   64 tokens  4096 -> 16384            16, 8        37.8       32, 4        25.7
+//              64 experts 1024 -> 4096  16, 8       280         32, 2        96.4 (32, 4: 110)
 void launch_gemm_weight_only(const WeightOnlyArgs& a, hipStream_t stream) {
     // Tokens that a workgroup should be ready for: all, or of an expert twice the
     // mean (more than that take the weights a second time).
     const int64_t each = !a.offsets ? a.rows : a.rows <= a.experts / 4 ? 1 : 2 * ((a.rows + a.experts - 1) / a.experts);
-    // Workgroups that 16 rows of W each would make.  Rows of W are joined, which
-    // halves the reads of the tokens, while two workgroups per CU are left.
+    // Workgroups that 16 rows of W each would make.
     const int64_t blocks = a.offsets ? (a.experts < a.rows ? a.experts : a.rows) : (a.rows + 63) / 64;
     const int64_t groups = (a.N + 15) / 16 * blocks;
     if (each == 1) {
         if (groups >= 1024 && a.K <= 5120) launch_one<16, 4>(a, stream);
         else launch_one<16, 8>(a, stream);
     } else if (each <= 4) {
-        if (groups < 1024) launch_chunks<1, 4, 8>(a, stream);
+        if (groups < 512) launch_chunks<1, 4, 8>(a, stream);
+        else if (groups < 2048) launch_chunks<1, 4, 4>(a, stream);
         else if (a.K <= 1024) launch_chunks<2, 4, 2>(a, stream);
-        else if (a.K <= 2560) launch_chunks<2, 4, 4>(a, stream);
-        else launch_chunks<2, 4, 8>(a, stream);
+        else launch_chunks<2, 4, 4>(a, stream);
     } else if (each <= 16) {
         if (groups < 512) launch_chunks<1, 16, 8>(a, stream);
-        else if (groups < 1024) launch_chunks<2, 16, 8>(a, stream);
-        else if (a.K <= 1024) launch_chunks<4, 16, 2>(a, stream);
-        else if (a.K <= 2560) launch_chunks<4, 16, 4>(a, stream);
-        else launch_chunks<4, 16, 8>(a, stream);
+        else if (groups < 1024) launch_chunks<1, 16, 4>(a, stream);
+        else if (groups >= 2048 && a.K <= 1024) launch_chunks<4, 16, 2>(a, stream);
+        else launch_chunks<2, 16, 4>(a, stream);
     } else if (each <= 32) {
-        if (groups < 512 || (groups < 1024 && a.K > 5120)) launch<1, 32, 8>(a, stream);
-        else if (groups < 1024) launch<1, 32, 4>(a, stream);
-        else if (a.K <= 1024 && groups >= 4096) launch<2, 32, 2>(a, stream);
-        else if (a.K <= 5120) launch<2, 32, 4>(a, stream);
-        else launch<2, 32, 8>(a, stream);
+        if (groups < 512) launch<1, 32, 8>(a, stream);
+        else if (groups >= 4096 && a.K <= 1024) launch<2, 32, 2>(a, stream);
+        else launch<2, 32, 4>(a, stream);
     } else {
         if (groups < 512) launch<1, 64, 8>(a, stream);
-        else if (a.K <= 1024 && groups >= 4096) launch<2, 64, 2>(a, stream);
-        else if (a.K <= 5120) launch<2, 64, 4>(a, stream);
-        else launch<2, 64, 8>(a, stream);
+        else if (groups >= 4096 && a.K <= 1024) launch<2, 64, 2>(a, stream);
+        else launch<2, 64, 4>(a, stream);
     }
 }
 

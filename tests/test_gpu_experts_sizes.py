@@ -127,7 +127,8 @@ def test_wgrad_in_many_tiles(cuda_device, M, N, bf16):
 
 @pytest.mark.parametrize("K", [16, 512, 528, 1152, 4224, 5648])
 @pytest.mark.parametrize("rows,N", [(1, 16), (1, 8209), (2, 16389), (4, 700), (9, 8195), (16, 16400), (16, 330), (31, 16390),
-                                    (32, 330), (33, 8195), (64, 650), (65, 650), (200, 4099), (20, 8200), (20, 65540), (40, 65540)])
+                                    (32, 330), (33, 8195), (64, 650), (65, 650), (200, 4099), (20, 8200), (20, 65540), (40, 65540),
+                                    (3, 32777), (9, 32777)])
 def test_weight_only_variants(cuda_device, rows, N, K):
     import torch
 
