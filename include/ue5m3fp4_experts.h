@@ -26,10 +26,10 @@
  * and GEMM steps are 128 deep, so expert g's rows stand in a transposed
  * operand (cols x rows_padded) from column
  *     p_g = 128 * (ceil(offsets[g] / 128) + g)
- * on, followed by quantized zeros (codes and scales 0 under any tensor scale but
- * 0 and NaN) up to the next multiple of 128 columns; rows_padded = 128 * (ceil(rows / 128) + experts).  Columns of no
- * expert are neither written nor read.  In other words: inside these column
- * ranges the operand is the transposed output of ue5m3fp4_quantize_blockscale
+ * on, followed by quantized zeros (codes and scales 0 under any tensor scale
+ * but 0 and NaN) up to the next multiple of 128 columns; rows_padded = 128 *
+ * (ceil(rows / 128) + experts).  Columns of no expert are neither written nor
+ * read.  In other words: inside these column ranges the operand is the transposed output of ue5m3fp4_quantize_blockscale
  * for the rows_padded x cols matrix that holds the experts' rows at their p_g
  * and zeros elsewhere (stochastic rounding draws for that matrix too).
  *

@@ -40,6 +40,8 @@ Pin status (see tests/test_oracle_*.py):
   gemm.py         pinned: exact rational triple loop on tiny shapes, an exact
                   integer special case.
   tensor_scale.py pinned: closed-form state machine cases.
+  experts.py      pinned: the definitions for one matrix on each expert's rows,
+                  worked layouts, exact rational loops.
 """
 
 from . import formats, philox, quantize, gemm, tensor_scale  # noqa: F401

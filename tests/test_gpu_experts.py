@@ -509,3 +509,35 @@ def test_gradients_against_differences(cuda_device):
             b, n = ox.spans(off)[e][:2]
             assert abs(float(host(dw)[e, i, j]) - want) <= 0.5 * (np.abs(G[b:b + n, i]) * np.abs(X[b:b + n, j])).sum()
     assert (host(dw)[1] == 0).all()
+
+
+def test_readme_examples(cuda_device):
+    """The README's blocks run in their order; the experts' results are those of their operands' values."""
+    import os
+
+    import torch
+
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    ns = {}
+    for block in text.split("```python\n")[1:]:
+        exec(compile(block.split("```")[0], "README.md", "exec"), ns)
+    torch.cuda.synchronize()
+
+    def value(q):
+        return lib.dequantize(q, torch.empty((q.rows, q.cols), dtype=torch.float32, device="cuda")).double()
+
+    def check(out, a, b, bf16):
+        ref, bound = a @ b.t(), 1e-5 * (a.abs() @ b.abs().t())
+        assert bool(((out.double() - ref).abs() <= (bound + 2.0 ** -8 * (ref.abs() + bound) if bf16 else bound)).all())
+
+    off = ns["offsets"].tolist()
+    x, xt, g, gt = value(ns["Xe"][0]), value(ns["Xe"][1]), value(ns["Ge"][0]), value(ns["Ge"][1])
+    for e in range(ns["experts"]):
+        b, n = off[e], off[e + 1] - off[e]
+        p, w = 128 * (-(-b // 128) + e), value(ns["We"].expert(e))
+        check(ns["ye"][b:b + n], x[b:b + n], w, True)
+        check(ns["dxe"][b:b + n], g[b:b + n], value(ns["WeT"].expert(e)), False)
+        check(ns["dwe"][e], gt[:, p:p + -(-n // 128) * 128], xt[:, p:p + -(-n // 128) * 128], False)
+    assert float(ns["yamax"]) == float(ns["ye"].float().abs().max())
+    check(ns["y1"], ns["x"][:1].double(), value(ns["W"][0]), True)
+    check(ns["y64"], ns["some"].double(), value(ns["We"].expert(0)), True)
