@@ -14,6 +14,7 @@ constexpr int64_t kMaxExperts = 65536;
 constexpr int64_t kMaxK = (int64_t)1 << 24;  // of a product: offsets inside a tile fit 32 bits
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned8(const void* p) { return ((uintptr_t)p & 7u) == 0; }
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 bool is01(int v) { return v == 0 || v == 1; }
 
@@ -75,8 +76,9 @@ int ue5m3fp4_gemm_grouped_nt(const uint8_t* a_codes, const uint8_t* a_scales, co
     if (experts == 0 || rows == 0 || N == 0) return UE5M3FP4_OK;  // nothing is read or written
     if (!a_ts || !b_ts || !offsets || !c) return UE5M3FP4_EINVAL;
     if (K > 0 && (!a_codes || !a_scales || !b_codes || !b_scales)) return UE5M3FP4_EINVAL;
-    if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(b_codes) || !aligned16(b_scales) || !aligned16(c) ||
-        !aligned4(a_ts) || !aligned4(b_ts) || !aligned4(offsets) || !aligned4(amax_inout))
+    // weights may begin at any expert of a larger operand, its scales so anywhere, unless K is a multiple of 128
+    if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned8(b_codes) || (K % 128 == 0 && !aligned8(b_scales)) ||
+        !aligned16(c) || !aligned4(a_ts) || !aligned4(b_ts) || !aligned4(offsets) || !aligned4(amax_inout))
         return UE5M3FP4_EALIGN;
     const GemmGroupedArgs g{a_codes, a_scales, a_ts, b_codes,      b_scales, b_ts,
                             b_ts_count == 1 ? 0 : 1, offsets, (int)experts, rows,     0, N,
@@ -124,8 +126,7 @@ int ue5m3fp4_gemm_weight_only(const uint16_t* x, int64_t ldx, const uint8_t* w_c
     if (K > 0 && (!x || !w_codes || !w_scales)) return UE5M3FP4_EINVAL;
     if (ldx < K || ldo < N) return UE5M3FP4_ESHAPE;
     if (ldx % 8 != 0) return UE5M3FP4_EALIGN;
-    if (!aligned16(x) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(out) || !aligned4(w_ts) ||
-        !aligned4(offsets))
+    if (!aligned16(x) || !aligned8(w_codes) || !aligned16(out) || !aligned4(w_ts) || !aligned4(offsets))
         return UE5M3FP4_EALIGN;
     const WeightOnlyArgs a{x,    ldx, w_codes, w_scales, w_ts, w_ts_count == 1 ? 0 : 1, offsets, (int)experts,
                            rows, N,   K,       out,      out_type == UE5M3FP4_OUT_BF16, ldo};

@@ -77,7 +77,8 @@ class ExpertWeights:
         return self.codes.shape[0]
 
     def expert(self, g):
-        """Expert g's operand (views), e.g. as an output of quantize_blockscale."""
+        """Expert g's operand (views), for gemm_weight_only, and as an output of quantize_blockscale or an operand of
+        the other products where R * C / 16 is a multiple of 16 (they need 16-byte aligned scales)."""
         return Quantized(self.codes[g], self.scales[g], self.ts[g:g + 1] if self.ts.numel() > 1 else self.ts)
 
 

@@ -29,18 +29,21 @@
  * on, followed by quantized zeros (codes and scales 0 under any tensor scale
  * but 0 and NaN) up to the next multiple of 128 columns; rows_padded = 128 *
  * (ceil(rows / 128) + experts).  Columns of no expert are neither written nor
- * read.  In other words: inside these column ranges the operand is the transposed output of ue5m3fp4_quantize_blockscale
- * for the rows_padded x cols matrix that holds the experts' rows at their p_g
- * and zeros elsewhere (stochastic rounding draws for that matrix too).
+ * read.  In other words: inside these column ranges the operand is the
+ * transposed output of ue5m3fp4_quantize_blockscale for the rows_padded x cols
+ * matrix that holds the experts' rows at their p_g and zeros elsewhere
+ * (stochastic rounding draws for that matrix too).
  *
  * Expert weights.  codes [experts][R][C / 2], scales [experts][R][C / 16],
- * and one tensor scale for all experts or one for each.
+ * and one tensor scale for all experts or one for each.  They may be some
+ * experts of a larger operand: codes have to be 8-byte aligned, scales 8-byte
+ * where C is a multiple of 128, else not at all.
  *
  * Conventions: those of include/ue5m3fp4.h -- device pointers owned by the
  * caller, every argument checked on the host before any HIP call, work
  * enqueued on `stream` of the current device, nothing allocated, synchronized
- * or kept; array base pointers 16-byte aligned, scalars, offsets and indices
- * 4-byte aligned; sizes of 0 are valid and launch nothing (except GEMMs with
+ * or kept; other array base pointers 16-byte aligned, scalars, offsets and
+ * indices 4-byte aligned; sizes of 0 are valid and launch nothing (except GEMMs with
  * an empty contraction, which write zeros).  At most 65536 experts (ERANGE).
  */
 #ifndef UE5M3FP4_EXPERTS_H

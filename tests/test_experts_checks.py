@@ -69,7 +69,8 @@ def test_gemm_argument_checks(L):
     assert gr(L, ct=2) == EINVAL and gr(L, n=3) == EINVAL and gr(L, n=0) == EINVAL and gr(L, ct=1, am=P) == EINVAL
     for name in ("ac", "as_", "at", "bc", "bs", "bt", "off", "c"):
         assert gr(L, **{name: None}) == EINVAL
-        assert gr(L, **{name: P + 2}) == EALIGN
+        assert gr(L, **{name: P + 2}, K=128) == EALIGN
+    assert gr(L, bc=P + 4) == EALIGN and gr(L, bs=P + 4, K=256) == EALIGN and gr(L, as_=P + 8) == EALIGN
     assert gr(L, am=P + 2) == EALIGN and gr(L, c=P + 4) == EALIGN
     assert gr(L, K=40) == ESHAPE
     assert gr(L, rows=1 << 31) == ERANGE and gr(L, N=1 << 31) == ERANGE and gr(L, K=1 << 24) == ERANGE
@@ -103,7 +104,8 @@ def test_weight_only_argument_checks(L):
     assert wo(L, n=3) == EINVAL and wo(L, n=0) == EINVAL
     for name in ("x", "wc", "ws", "wt", "out"):
         assert wo(L, **{name: None}) == EINVAL
-        assert wo(L, **{name: P + 2}) == EALIGN
+        assert name == "ws" or wo(L, **{name: P + 2}) == EALIGN
+    assert wo(L, wc=P + 4) == EALIGN and wo(L, x=P + 8) == EALIGN and wo(L, out=P + 8) == EALIGN
     assert wo(L, off=P + 2) == EALIGN and wo(L, ldx=36) == EALIGN
     assert wo(L, K=40, ldx=40) == ESHAPE and wo(L, ldx=24) == ESHAPE and wo(L, ldo=31) == ESHAPE
     assert wo(L, rows=1 << 31) == ERANGE and wo(L, K=1 << 24, ldx=1 << 24) == ERANGE and wo(L, ldx=1 << 39) == ERANGE and wo(L, ldo=1 << 39) == ERANGE

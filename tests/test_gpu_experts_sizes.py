@@ -179,6 +179,32 @@ def test_weight_only_largest_tokens(cuda_device, rows):
     check(out, x.double(), values(q), False)
 
 
+@pytest.mark.parametrize("N,K", [(37, 144), (45, 528), (1305, 2064), (35, 256)])
+def test_some_experts_of_a_larger_operand(cuda_device, N, K):
+    """Weights that begin at an expert of an operand whose scales have odd sizes: 8-byte aligned codes, scales anywhere."""
+    import torch
+
+    w = rand_weights(6, N, K, 30)
+    counts = [5, 130, 0, 66]
+    off, rows = dev_i32(offsets_of(counts)), sum(counts)
+    part = lib.ExpertWeights(w.codes[1:5], w.scales[1:5], w.ts[1:5])
+    alone = lib.ExpertWeights(part.codes.clone(), part.scales.clone(), part.ts.clone())
+    assert K == 256 or w.scales[1].data_ptr() % 16
+    a, x = rand_operand(rows, K, 31), torch.randn((rows, K), device="cuda", generator=gen(32)).bfloat16()
+    got, want = empty((rows, N), False), empty((rows, N), False)
+    lib.gemm_grouped_fprop(a, part, off, got)
+    lib.gemm_grouped_fprop(a, alone, off, want)
+    assert torch.equal(got, want)
+    check(got[5:135], values(a)[5:135], values(part.expert(1)), False)
+    lib.gemm_weight_only(x, part, got, offsets=off)
+    lib.gemm_weight_only(x, alone, want, offsets=off)
+    assert torch.equal(got, want)
+    for tokens in (1, 3, 16, 40):
+        y = empty((tokens, N), False)
+        lib.gemm_weight_only(x[:tokens], w.expert(3), y)
+        check(y, x[:tokens].double(), values(w.expert(3)), False)
+
+
 # ------------------------------------------------------------ large operands --
 
 def test_quantize_past_32_bit_offsets(cuda_device):
