@@ -9,10 +9,11 @@
 // rows_padded x cols matrix that the transposed operand is blocked along (each
 // expert's rows from a multiple of 128 on), so a tile has rows of one expert
 // and both outputs come from one read.  Which expert: the last whose first
-// padded row is not behind the tile's, counted by ballots over 64 experts at a
-// time in each wave, without a scan or a second kernel.  Tiles in the gaps end
-// there.  Rows of a tile behind the expert's last are zeros, which quantize to
-// the operand's padding.
+// padded row is not behind the tile's, found by ballots in each wave, among 64
+// ranges of experts and then in the range, without a scan or a second kernel (1024
+// experts, 4096 x 1024, mostly padding: 62 us, 64 experts after another 85).  Tiles in
+// the gaps end there.  Rows of a tile behind the expert's last are zeros, which
+// quantize to the operand's padding.
 //
 // Thread t loads 16-byte unit t % 32 (8 columns) of tile rows t / 32 + 8k, all
 // loads issued back to back; the row-wise pass quantizes from registers (a lane
@@ -108,24 +109,25 @@ __global__ __launch_bounds__(kThreads) void quantize_grouped_kernel(QuantizeGrou
 
     // ---- the tile's expert, and the grouped rows [row0, end) it has here
     const float ts = (ROW || COL) ? *a.tensor_scale : 0.0f;
-    int g = -1;
-    GroupRows own{0, 0};
-    for (int base = 0; base < a.experts; base += 64) {
-        GroupRows r{0, 0};
-        bool before = false;
-        if (base + lane < a.experts) {
-            r = group_rows(a.offsets, base + lane, (int)a.rows);
-            before = padded_begin(r.begin, base + lane) <= R0;
-        }
-        const uint64_t votes = __ballot(before);
-        if (votes == 0) break;
-        const int last = __popcll(votes) - 1;
-        g = base + last;
-        own.begin = __shfl(r.begin, last);
-        own.end = __shfl(r.end, last);
-        if (last < 63) break;
+    int low = 0, candidates = a.experts;
+    while (candidates > 64) {  // which of 64 ranges of experts
+        const int step = (candidates + 63) / 64, e = low + lane * step;
+        const bool before = lane * step < candidates && padded_begin(group_rows(a.offsets, e, (int)a.rows).begin, e) <= R0;
+        const int begun = (int)__popcll(__ballot(before)), last = begun > 0 ? begun - 1 : 0;
+        candidates = min(step, candidates - last * step);
+        low += last * step;
     }
-    if (g < 0) return;  // before the first expert's rows
+    GroupRows own{0, 0};
+    bool before = false;
+    if (lane < candidates) {
+        own = group_rows(a.offsets, low + lane, (int)a.rows);
+        before = padded_begin(own.begin, low + lane) <= R0;
+    }
+    const int last = __popcll(__ballot(before)) - 1;
+    if (last < 0) return;  // before the first expert's rows
+    const int g = low + last;
+    own.begin = __shfl(own.begin, last);
+    own.end = __shfl(own.end, last);
     const int64_t rel = R0 - padded_begin(own.begin, g);
     const int64_t end = own.end, row0 = own.begin + rel;
     // behind the expert's padding (or, for the row-wise output alone, its rows);

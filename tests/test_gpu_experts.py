@@ -541,3 +541,33 @@ def test_readme_examples(cuda_device):
     assert float(ns["yamax"]) == float(ns["ye"].float().abs().max())
     check(ns["y1"], ns["x"][:1].double(), value(ns["W"][0]), True)
     check(ns["y64"], ns["some"].double(), value(ns["We"].expert(0)), True)
+
+
+@pytest.mark.parametrize("experts", [65, 300, 4200])
+def test_many_experts(cuda_device, experts):
+    """More experts than one or two rounds of 64 ranges tell apart; few have rows."""
+    rng = np.random.default_rng(experts)
+    counts = np.where(rng.random(experts) < 0.05, rng.integers(1, 40, experts), 0)
+    counts[[0, -1]] = 3, 5
+    off = offsets_of(counts, 2)
+    rows, N, K = int(off[-1]) + 1, 24, 32
+    bits = random_bf16((rows, K), 6, "gradient")
+    ts, o = fresh_ts(bits), dev_i32(off)
+    tsd, amax = dev_scalar(ts), dev_scalar(0.0)
+    qr, qc = grouped_buffers(rows, K, experts, tsd)
+    lib.quantize_grouped(dev_bf16(bits), o, tsd, lib.SR, 5, 1, row=qr, col=qc, amax=amax)
+    check_row(qr, bits, off, ts, 1, 5, 1)
+    check_col(qc, bits, off, ts, 1, 5, 1)
+    assert host(amax)[0] == ox.amax(bits, off)
+    q = operand((N, K), 7)
+    bc, bs, bts = np.repeat(q[0][None], experts, 0), np.repeat(q[1][None], experts, 0), np.arange(1, experts + 1, dtype=np.float32)
+    import torch
+
+    w = lib.ExpertWeights(dev_u8(bc), dev_u8(bs), torch.from_numpy(bts).cuda())  # told apart by their tensor scales
+    a = quantize.quantize_blockscale(bits, ts)
+    y = empty_result((rows, N), False)
+    lib.gemm_grouped_fprop(dev_operand((*a, ts)), w, o, y)
+    check_result(y, *ox.gemm_rows(a, ts, bc, bs, bts, off))
+    y = empty_result((rows, N), False)
+    lib.gemm_weight_only(dev_bf16(bits), w, y, offsets=o)
+    check_result(y, *ox.weight_only(bits, bc, bs, bts, off))
