@@ -614,7 +614,9 @@ void launch(const WeightOnlyArgs& a, hipStream_t stream) {
 // workgroups.  Waves, which share out K: 8 have the most loads in flight where there are
 // few workgroups (16384 -> 4096, 4 tokens, 12.7 us, with 4 waves 16.5); where there are
 // many, fewer leave none idle when K is short and join fewer sums.  Measured, us:
-//   16 tokens  1024 -> 16384        16 rows, 8 waves  8.6   32 rows, 4 waves  6.8
+//   1 token    4096 -> 16384        16 rows, 8 waves  9.9   16 rows, 4 waves  8.7
+//              16 of 64 experts 1024 -> 4096  16, 8  21.1       16, 2        10.8 (16, 4: 13.1)
+//   16 tokens  1024 -> 16384            16, 8         8.6       32, 4         6.8
 //              9 experts 2064 -> 1305   32, 8        12.8       16, 4         9.0
 //              64 experts 4096 -> 2048  64, 8        92.6       32, 4        68.0
 //              64 experts 1024 -> 4096  16, 8       131         64, 2        43.9 (32, 4: 50.4)
@@ -628,7 +630,8 @@ void launch_gemm_weight_only(const WeightOnlyArgs& a, hipStream_t stream) {
     const int64_t blocks = a.offsets ? (a.experts < a.rows ? a.experts : a.rows) : (a.rows + 63) / 64;
     const int64_t groups = (a.N + 15) / 16 * blocks;
     if (each == 1) {
-        if (groups >= 1024 && a.K <= 5120) launch_one<16, 4>(a, stream);
+        if (groups >= 2048 && a.K <= 1024) launch_one<16, 2>(a, stream);
+        else if (groups >= 1024 && a.K <= 5120) launch_one<16, 4>(a, stream);
         else launch_one<16, 8>(a, stream);
     } else if (each <= 4) {
         if (groups < 512) launch_chunks<1, 4, 8>(a, stream);

@@ -124,7 +124,7 @@ def test_wgrad_in_many_tiles(cuda_device, M, N, bf16):
 # ---------------------------------------------------- the weight-only product --
 
 @pytest.mark.parametrize("K", [16, 512, 528, 1152, 4224, 5648])
-@pytest.mark.parametrize("rows,N", [(1, 16), (1, 8209), (2, 16389), (4, 700), (9, 8195), (16, 16400), (16, 330), (31, 16390),
+@pytest.mark.parametrize("rows,N", [(1, 16), (1, 8209), (1, 32790), (2, 16389), (4, 700), (9, 8195), (16, 16400), (16, 330), (31, 16390),
                                     (32, 330), (33, 8195), (64, 650), (65, 650), (200, 4099), (20, 8200), (20, 65540), (40, 65540),
                                     (3, 32777), (9, 32777)])
 def test_weight_only_variants(cuda_device, rows, N, K):
@@ -139,9 +139,10 @@ def test_weight_only_variants(cuda_device, rows, N, K):
         check(out, xv, qv, bf16)
 
 
-@pytest.mark.parametrize("K", [512, 400])
+@pytest.mark.parametrize("K", [512, 400, 1040])
 @pytest.mark.parametrize("counts,N", [
     ([1, 0, 0, 0, 0, 0, 1, 0], 1100),               # one token each
+    ([1, 0, 0, 0, 0, 0, 1, 0] * 8, 2100),
     ([3, 0, 4, 1, 2, 5] * 12, 260),                 # more experts than lanes of a wave, 1 more than is prepared for
     ([16, 1, 0, 9, 40] * 16, 330),                  # two row blocks of some
     ([33, 0, 31, 10] * 9, 460),
