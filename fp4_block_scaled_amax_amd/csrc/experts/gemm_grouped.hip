@@ -767,11 +767,16 @@ void launch_gemm_grouped_nt(const GemmGroupedArgs& g, hipStream_t stream) {
 }
 
 // The same rule: one expert of 2048 rows, 1024 x 1024, 22 -> 11 us split; 4 experts of
-// 512 rows, 1024 x 1024 (1024 tiles), would lose, 12 -> 16 us.
+// 512 rows, 1024 x 1024 (1024 tiles), would lose, 12 -> 16 us.  Tiles of 256 rows only
+// where they have work beside their first loads and their results: 16 experts of 256
+// rows, 2048 x 4096 (4096 tiles of 2 steps), 149 -> 137 us; 8 of 256, 2048 x 2048 (1024
+// of 2), would lose, 32 -> 37 us, and 16 of 64, 2048 x 4096 (4096 of 1), 104 -> 115 us.
 void launch_gemm_grouped_wgrad(const GemmGroupedArgs& g, hipStream_t stream) {
     auto tiles = [&](int rows, int cols) { return g.experts * ((g.M + rows - 1) / rows) * ((g.N + cols - 1) / cols); };
+    const int64_t steps = (g.rows / g.experts + kBK - 1) / kBK;  // of an expert with the mean number of rows
     if (tiles(kSplitRows, kSplitCols) <= kFew) launch_wgrad<kSplitRows, kSplitCols>(g, stream, gemm_grouped_wgrad_split_kernel);
-    else if (tiles(256, kBN) < kFew) launch_wgrad<128, kBN>(g, stream, gemm_grouped_wgrad_kernel<128>);
+    else if (steps < 2 || tiles(256, kBN) < kFew || tiles(256, kBN) * steps < 10 * kFew)
+        launch_wgrad<128, kBN>(g, stream, gemm_grouped_wgrad_kernel<128>);
     else launch_wgrad<256, kBN>(g, stream, gemm_grouped_wgrad_kernel<256>);
 }
 

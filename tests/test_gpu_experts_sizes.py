@@ -105,7 +105,7 @@ def test_grouped_rows_in_many_tiles(cuda_device, N, K, bf16):
 
 
 @pytest.mark.parametrize("bf16", [False, True])
-@pytest.mark.parametrize("M,N", [(2100, 1500), (2050, 1504), (1801, 2001), (700, 701), (720, 704), (130, 68), (33, 67)])
+@pytest.mark.parametrize("M,N", [(2100, 5000), (2050, 5104), (1801, 6001), (2100, 1500), (700, 701), (720, 704), (130, 68), (33, 67)])
 def test_wgrad_in_many_tiles(cuda_device, M, N, bf16):
     counts = [0, 1, 300, 128, 1165]
     off, E = offsets_of(counts, 2), len(counts)
