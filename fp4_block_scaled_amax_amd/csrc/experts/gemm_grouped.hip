@@ -25,6 +25,8 @@
 // rows go in tiles of full height while more than half of one is left, and the rest
 // in one lower tile.  Full tiles are dealt first, the rests after them: the short
 // ones fill what the last round of long ones leaves.
+// Where that makes too few tiles for 256 CUs, 64 x 64 results whose contraction the
+// waves share out.
 #include "../formats.hpp"
 #include "experts.hpp"
 
@@ -116,11 +118,13 @@ __device__ __forceinline__ void put(uint16_t& to, float v, uint32_t& tmax) {
 // pieces of rows (bf16; 128 in fp32), and that bounds wide and short products; so
 // each 32 rows pass through this wave's part of the staging buffers, which no one
 // needs any more, and leave in 16 bytes per lane, whole rows of the wave's tile at a
-// time: 16384 x 32768 results of bf16 stored alone
-// take 255 us so, and 561 us without.  Where rows of C do not begin at
-// multiples of 16 bytes they are stored directly.  Returns the largest magnitude of
-// what bf16 stores hold; rows and columns past the tile repeat its last ones, so
-// they need no exception.
+// time: 16384 x 32768 results of bf16 stored alone take 255 us so, and 561 us without.
+// They pass the caches, which then keep the operands (wgrad of 64 experts of 256 rows,
+// 2048 x 4096, 594 -> 451 us).  Where rows of C do not begin at multiples of 16 bytes
+// they are stored directly, in pieces that the caches join (past them 7 experts of 219
+// rows, 2064 x 1305, would take 38 us instead of 26).  Returns the largest magnitude of
+// what bf16 stores hold; rows and columns past the tile repeat its last ones, so they
+// need no exception.
 template <typename L, int RI, int CJ, typename OUT>
 __device__ __forceinline__ uint32_t store_tile(const f32x16_t (&acc)[RI][CJ], const Tile& t, uint8_t* smem, OUT* C,
                                                int64_t N, int wm, int wn) {
@@ -147,7 +151,7 @@ __device__ __forceinline__ uint32_t store_tile(const f32x16_t (&acc)[RI][CJ], co
                 const int row = m * (64 / kLanes) + lane / kLanes, col = lane % kLanes * kPer;
                 const u32x4 v = *reinterpret_cast<const u32x4*>(mine + row * kStride + col * sizeof(OUT));
                 if (row0 + 32 * i + row < t.rows && col0 + col < t.cols)
-                    *reinterpret_cast<u32x4*>(C + (row0 + 32 * i + row) * N + col0 + col) = v;
+                    __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(C + (row0 + 32 * i + row) * N + col0 + col));
             }
             wave_sync();
         }
