@@ -283,7 +283,7 @@ def gemm_weight_only(x, w, out, offsets=None, stream=None):
     """out [rows][N] (bf16 or fp32, unit column stride) = x W^T with x [rows][K]
     in bf16 and FP4 weights: w a Quantized [N][K], or with offsets the
     ExpertWeights [experts][N][K] of the rows' experts.  Made for few rows (1 to
-    about 64 per expert)."""
+    about 64 per expert).  Rows of no expert keep what they held."""
     import torch
 
     rows, K, ldx, device = _rows(x, (torch.bfloat16, torch.int16, torch.uint16), "x")
