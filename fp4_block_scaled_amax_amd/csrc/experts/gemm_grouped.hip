@@ -385,10 +385,13 @@ __device__ __forceinline__ void compute_tile(const Tile& t, uint8_t* smem, const
     if (g.amax) amax_commit(tmax, g.amax);
 }
 
+// The lowest tile that holds the rows: 64 unequal experts of 256 rows on average, 2048 ->
+// 4096, 310 us, without the one of 192 rows 324.
 template <int BM, bool WHOLE>
 __device__ __forceinline__ void compute(const Tile& t, uint8_t* smem, const GemmGroupedArgs& g) {
     if constexpr (BM == 256) {
-        if (t.rows > 128) return compute_tile<BM, 4, 2, 2, 2, WHOLE>(t, smem, g);
+        if (t.rows > 192) return compute_tile<BM, 4, 2, 2, 2, WHOLE>(t, smem, g);
+        if (t.rows > 128) return compute_tile<BM, 3, 2, 2, 2, WHOLE>(t, smem, g);
     }
     if (t.rows > 64) compute_tile<BM, 2, 2, 2, 2, WHOLE>(t, smem, g);
     else if (t.rows > 32) compute_tile<BM, 1, 2, 2, 2, WHOLE>(t, smem, g);

@@ -83,7 +83,7 @@ def check(out, a, b, bf16):
 
 # Tiles of 256 rows (N 8200), of 128 (N 700) and of 64 with split contractions (N 100).
 # Behind full tiles: rests of 1 .. 32, 33 .. 64, 65 .. 128 and 129 .. 255, and none
-TALL = [256, 1, 33, 65, 129, 257, 300, 384, 385, 0, 511, 512]
+TALL = [256, 1, 33, 65, 129, 257, 300, 384, 385, 0, 511, 512, 192, 193, 440]
 
 
 @pytest.mark.parametrize("bf16", [False, True])
