@@ -521,8 +521,8 @@ __global__ __launch_bounds__(64 * WAVES, RT > 2 ? 2 : RT * TOKENS >= 32 ? 3 : 4)
                 for (int s = 0; s < PART; ++s)
 #pragma unroll
                     for (int u = 0; u < 4; ++u) xf[s][u] = fragment(s, u);
-                lds_reads_done();
             }
+            lds_reads_done();  // of the place that is loaded next: just now, or (two places) a turn ago
             const bool last = part == 4 / PART - 1;
             const uint32_t kx = last ? next : k0 + 128 * PART * (part + 1);
             if (kx < K) load_tokens(kx, xs_at + (kPlaces - 1) * (at ^ 1) * (PART * kStepBytes));
