@@ -89,6 +89,14 @@ __device__ __forceinline__ int64_t padded_begin(int begin, int g) {
     return 128 * (((int64_t)begin + 127) / 128 + g);
 }
 
+// sum + part; returns what that rounds off, which belongs to the next part (nothing of an
+// infinity or NaN).
+__device__ __forceinline__ float fold(float& sum, float part) {
+    const float s = sum + part, b = s - sum, lost = (sum - (s - b)) + (part - b);
+    sum = s;
+    return s - s == 0.0f ? lost : 0.0f;
+}
+
 // Inclusive sum over the lanes of a wave.
 __device__ __forceinline__ int wave_scan(int v) {
     const int lane = threadIdx.x & 63;

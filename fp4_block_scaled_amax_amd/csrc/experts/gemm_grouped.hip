@@ -45,6 +45,16 @@ constexpr int kBK = 128;
 constexpr int kThreads = 256;
 constexpr int kGroupM = 4;  // tile rows that are walked together
 
+// A sum takes up to kChain steps (32768 elements, 2048 matrix instructions), each of
+// which rounds it.  Where the terms are alike the roundings go one way: rows of one
+// or two values each were off by up to 8e-6 of sum |a b| at 8192 elements, 4e-5 at 32768, 1e-4 at
+// 65536 and 3e-3 at 2^21, random terms of one sign by 1e-6, 3e-6, 3e-6 and 3e-5.  Longer
+// ones (LONG) are joined from sums of kFold steps, and what a join rounds off begins
+// the next one, so that length adds nothing: 4e-6 at any.  That needs a second register
+// for each sum, so such tiles have 128 rows: one expert's wgrad over 131072 rows, 4096 x
+// 4096, 4.50 ms, 3.76 without; experts with shorter contractions beside it lose nothing.
+constexpr int kChain = 256, kFold = 32;
+
 // UE5M3 byte -> expanded dword (0xFF: m = NaN, which poisons what it enters).
 __device__ __forceinline__ uint32_t expand_scale(uint32_t c) {
     const uint32_t e = c >> 3, f = c & 7u;
@@ -222,6 +232,29 @@ __device__ __forceinline__ uint32_t load_scales(const uint8_t* row, uint32_t blo
     return w;
 }
 
+template <int RI, int CJ>
+__device__ __forceinline__ void fold_all(f32x16_t (&acc)[RI][CJ], f32x16_t (&sum)[RI][CJ]) {
+#pragma unroll
+    for (int i = 0; i < RI; ++i)
+#pragma unroll
+        for (int j = 0; j < CJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                float s = sum[i][j][e];
+                acc[i][j][e] = fold(s, acc[i][j][e]);
+                sum[i][j][e] = s;
+            }
+}
+template <int RI, int CJ>
+__device__ __forceinline__ void add_all(f32x16_t (&acc)[RI][CJ], const f32x16_t (&sum)[RI][CJ]) {
+#pragma unroll
+    for (int i = 0; i < RI; ++i)
+#pragma unroll
+        for (int j = 0; j < CJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = sum[i][j][e] + acc[i][j][e];
+}
+
 // One tile of 32 RI WM rows x 128 columns, by WM x WN waves of RI x CJ 32 x 32
 // results.
 //
@@ -236,7 +269,7 @@ __device__ __forceinline__ uint32_t load_scales(const uint8_t* row, uint32_t blo
 // step: 2 units, 4 blocks, 8 matrix instructions.  A and B agree on it, so the sums
 // are those of the plain order.  A scale byte is expanded where it is used: 16 rows'
 // bytes mostly name few table entries.
-template <int BM, int RI, int CJ, int WM, int WN, bool WHOLE>
+template <int BM, int RI, int CJ, int WM, int WN, bool WHOLE, bool LONG>
 __device__ __forceinline__ void compute_tile(const Tile& t, uint8_t* smem, const GemmGroupedArgs& g) {
     using L = Lds<BM>;
     constexpr int kRowsA = 32 * RI * WM;
@@ -314,13 +347,16 @@ __device__ __forceinline__ void compute_tile(const Tile& t, uint8_t* smem, const
 
     const int row_a = wm * 32 * RI + r, row_b = wn * 32 * CJ + r;
     const int swizzle_a = (row_a >> 2) & 3, swizzle_b = (row_b >> 2) & 3;  // rows 32 apart have the same
-    f32x16_t acc[RI][CJ];
+    f32x16_t acc[RI][CJ], sum[LONG ? RI : 1][LONG ? CJ : 1];
 #pragma unroll
     for (int i = 0; i < RI; ++i)
 #pragma unroll
         for (int j = 0; j < CJ; ++j)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+            for (int e = 0; e < 16; ++e) {
+                acc[i][j][e] = 0.0f;
+                if constexpr (LONG) sum[i][j][e] = 0.0f;
+            }
 
     if (steps > 0) {
         stage(0, 0);
@@ -374,7 +410,10 @@ __device__ __forceinline__ void compute_tile(const Tile& t, uint8_t* smem, const
         }
         if constexpr (!WHOLE)
             if (step + 1 < steps) put_scales((step + 1) & 1);
+        if constexpr (LONG)
+            if (step % kFold == kFold - 1) fold_all(acc, sum);
     }
+    if constexpr (LONG) add_all(acc, sum);
     step_ready();  // all waves are past their last step: the stages are free
 
     // Epilogue: accumulator e of lane (r, h) is row 8 (e / 4) + 4 h + e % 4, column
@@ -387,15 +426,30 @@ __device__ __forceinline__ void compute_tile(const Tile& t, uint8_t* smem, const
 
 // The lowest tile that holds the rows: 64 unequal experts of 256 rows on average, 2048 ->
 // 4096, 310 us, without the one of 192 rows 324.
-template <int BM, bool WHOLE>
+template <int BM, bool WHOLE, bool LONG>
 __device__ __forceinline__ void compute(const Tile& t, uint8_t* smem, const GemmGroupedArgs& g) {
-    if constexpr (BM == 256) {
-        if (t.rows > 192) return compute_tile<BM, 4, 2, 2, 2, WHOLE>(t, smem, g);
-        if (t.rows > 128) return compute_tile<BM, 3, 2, 2, 2, WHOLE>(t, smem, g);
+    if constexpr (BM == 256 && !LONG) {
+        if (t.rows > 192) return compute_tile<BM, 4, 2, 2, 2, WHOLE, LONG>(t, smem, g);
+        if (t.rows > 128) return compute_tile<BM, 3, 2, 2, 2, WHOLE, LONG>(t, smem, g);
     }
-    if (t.rows > 64) compute_tile<BM, 2, 2, 2, 2, WHOLE>(t, smem, g);
-    else if (t.rows > 32) compute_tile<BM, 1, 2, 2, 2, WHOLE>(t, smem, g);
-    else compute_tile<BM, 1, 1, 1, 4, WHOLE>(t, smem, g);
+    if (t.rows > 64) compute_tile<BM, 2, 2, 2, 2, WHOLE, LONG>(t, smem, g);
+    else if (t.rows > 32) compute_tile<BM, 1, 2, 2, 2, WHOLE, LONG>(t, smem, g);
+    else compute_tile<BM, 1, 1, 1, 4, WHOLE, LONG>(t, smem, g);
+}
+
+// A tile with a long contraction, 128 of its rows at a time.
+template <int BM>
+__device__ __forceinline__ void compute_long(const Tile& t, uint8_t* smem, const GemmGroupedArgs& g) {
+#pragma unroll 1
+    for (int m = 0; m < t.rows; m += 128) {
+        Tile part = t;
+        part.a += m * t.a_stride;
+        part.as += m * t.as_stride;
+        part.c += m * g.N;
+        part.rows = min(t.rows - m, 128);
+        if (m > 0) step_ready();  // the results before have left their place in LDS
+        compute<BM, true, true>(part, smem, g);
+    }
 }
 
 // ---- few tiles: the waves of a workgroup share out the contraction
@@ -422,7 +476,7 @@ struct Step {
     u32x4 ca[RI][2], cb[CJ][2];
     uint32_t sa[RI], sb[CJ];
 };
-template <int RI, int CJ, bool WHOLE>
+template <int RI, int CJ, bool WHOLE, bool LONG>
 __device__ __forceinline__ void split_tile(const Tile& t, uint8_t* smem, const GemmGroupedArgs& g) {
     using L = SplitLds;
     const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
@@ -467,13 +521,16 @@ __device__ __forceinline__ void split_tile(const Tile& t, uint8_t* smem, const G
             }
         }
     };
-    f32x16_t acc[RI][CJ];
+    f32x16_t acc[RI][CJ], sum[LONG ? RI : 1][LONG ? CJ : 1];
 #pragma unroll
     for (int i = 0; i < RI; ++i)
 #pragma unroll
         for (int j = 0; j < CJ; ++j)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+            for (int e = 0; e < 16; ++e) {
+                acc[i][j][e] = 0.0f;
+                if constexpr (LONG) sum[i][j][e] = 0.0f;
+            }
 
     Step<RI, CJ> next;
     if (wave * kBK < K) load(next, wave * kBK);
@@ -505,7 +562,10 @@ __device__ __forceinline__ void split_tile(const Tile& t, uint8_t* smem, const G
                 }
             }
         }
+        if constexpr (LONG)
+            if (k / (kSplit * kBK) % kFold == kFold - 1) fold_all(acc, sum);
     }
+    if constexpr (LONG) add_all(acc, sum);
 
     // ---- the waves' sums: accumulator e of lane (r, h) is row 8 (e / 4) + 4 h + e % 4,
     // column r of its 32 x 32 tile
@@ -689,45 +749,49 @@ __device__ __forceinline__ void wgrad_tile(const GemmGroupedArgs& g, Tile& t) {
     t.sb = *g.b_ts;
 }
 
-template <int BM, bool WHOLE>
+template <int BM, bool WHOLE, bool LONG>
 __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_nt_kernel(GemmGroupedArgs g) {
     using L = Lds<BM>;
     __shared__ __align__(16) uint8_t smem[L::kBytes];
     Tile t;
     if (!nt_tile<BM, kBN>(g, t)) return;
     reinterpret_cast<uint32_t*>(smem + L::kLut)[threadIdx.x] = expand_scale(threadIdx.x);
-    compute<BM, WHOLE>(t, smem, g);
+    compute<BM, WHOLE, LONG>(t, smem, g);
 }
 
-template <int BM>
+// LONG: an expert may have more than kChain steps of rows.
+template <int BM, bool LONG>
 __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_wgrad_kernel(GemmGroupedArgs g) {
     using L = Lds<BM>;
     __shared__ __align__(16) uint8_t smem[L::kBytes];
     reinterpret_cast<uint32_t*>(smem + L::kLut)[threadIdx.x] = expand_scale(threadIdx.x);
     Tile t;
     wgrad_tile<BM, kBN>(g, t);
-    compute<BM, true>(t, smem, g);
+    if constexpr (LONG)
+        if (t.K > kChain * kBK) return compute_long<BM>(t, smem, g);
+    compute<BM, true, false>(t, smem, g);
 }
 
-template <bool WHOLE>
+template <bool WHOLE, bool LONG>
 __device__ __forceinline__ void split(const Tile& t, uint8_t* smem, const GemmGroupedArgs& g) {
     reinterpret_cast<uint32_t*>(smem + SplitLds::kLut)[threadIdx.x] = expand_scale(threadIdx.x);
-    if (t.rows > 32) split_tile<2, 2, WHOLE>(t, smem, g);
-    else split_tile<1, 2, WHOLE>(t, smem, g);
+    if (t.rows > 32) split_tile<2, 2, WHOLE, LONG>(t, smem, g);
+    else split_tile<1, 2, WHOLE, LONG>(t, smem, g);
 }
 
-template <bool WHOLE>
-__global__ __launch_bounds__(kThreads, 2) void gemm_grouped_nt_split_kernel(GemmGroupedArgs g) {
+template <bool WHOLE, bool LONG>
+__global__ __launch_bounds__(kThreads, LONG && !WHOLE ? 1 : 2) void gemm_grouped_nt_split_kernel(GemmGroupedArgs g) {
     __shared__ __align__(16) uint8_t smem[SplitLds::kBytes];
     Tile t;
-    if (nt_tile<kSplitRows, kSplitCols>(g, t)) split<WHOLE>(t, smem, g);
+    if (nt_tile<kSplitRows, kSplitCols>(g, t)) split<WHOLE, LONG>(t, smem, g);
 }
 
+template <bool LONG>
 __global__ __launch_bounds__(kThreads, 2) void gemm_grouped_wgrad_split_kernel(GemmGroupedArgs g) {
     __shared__ __align__(16) uint8_t smem[SplitLds::kBytes];
     Tile t;
     wgrad_tile<kSplitRows, kSplitCols>(g, t);
-    split<true>(t, smem, g);
+    split<true, LONG>(t, smem, g);
 }
 
 template <int BM, int BN, typename KERNEL>
@@ -762,9 +826,12 @@ void dispatch_nt(const GemmGroupedArgs& g, hipStream_t stream) {
     // tiles that experts with the mean number of rows make
     const int64_t some = g.experts < g.rows ? g.experts : g.rows, each = (g.rows + some - 1) / some;
     auto tiles = [&](int rows, int cols) { return some * ((each + rows - 1) / rows) * ((g.N + cols - 1) / cols); };
-    if (tiles(kSplitRows, kSplitCols) <= kFew) launch_nt<kSplitRows, kSplitCols>(g, stream, gemm_grouped_nt_split_kernel<WHOLE>);
-    else if (tiles(256, kBN) < kFew) launch_nt<128, kBN>(g, stream, gemm_grouped_nt_kernel<128, WHOLE>);
-    else launch_nt<256, kBN>(g, stream, gemm_grouped_nt_kernel<256, WHOLE>);
+    if (tiles(kSplitRows, kSplitCols) <= kFew) {
+        if (g.K > kSplit * kChain * kBK) launch_nt<kSplitRows, kSplitCols>(g, stream, gemm_grouped_nt_split_kernel<WHOLE, true>);
+        else launch_nt<kSplitRows, kSplitCols>(g, stream, gemm_grouped_nt_split_kernel<WHOLE, false>);
+    } else if (g.K > kChain * kBK) launch_nt<128, kBN>(g, stream, gemm_grouped_nt_kernel<128, WHOLE, true>);
+    else if (tiles(256, kBN) < kFew) launch_nt<128, kBN>(g, stream, gemm_grouped_nt_kernel<128, WHOLE, false>);
+    else launch_nt<256, kBN>(g, stream, gemm_grouped_nt_kernel<256, WHOLE, false>);
 }
 
 }  // namespace
@@ -781,10 +848,17 @@ void launch_gemm_grouped_nt(const GemmGroupedArgs& g, hipStream_t stream) {
 void launch_gemm_grouped_wgrad(const GemmGroupedArgs& g, hipStream_t stream) {
     auto tiles = [&](int rows, int cols) { return g.experts * ((g.M + rows - 1) / rows) * ((g.N + cols - 1) / cols); };
     const int64_t steps = (g.rows / g.experts + kBK - 1) / kBK;  // of an expert with the mean number of rows
-    if (tiles(kSplitRows, kSplitCols) <= kFew) launch_wgrad<kSplitRows, kSplitCols>(g, stream, gemm_grouped_wgrad_split_kernel);
-    else if (steps < 2 || tiles(256, kBN) < kFew || tiles(256, kBN) * steps < 10 * kFew)
-        launch_wgrad<128, kBN>(g, stream, gemm_grouped_wgrad_kernel<128>);
-    else launch_wgrad<256, kBN>(g, stream, gemm_grouped_wgrad_kernel<256>);
+    const int64_t most = (g.rows + kBK - 1) / kBK;  // steps of an expert with all rows
+    if (tiles(kSplitRows, kSplitCols) <= kFew) {
+        if (most > kSplit * kChain) launch_wgrad<kSplitRows, kSplitCols>(g, stream, gemm_grouped_wgrad_split_kernel<true>);
+        else launch_wgrad<kSplitRows, kSplitCols>(g, stream, gemm_grouped_wgrad_split_kernel<false>);
+    } else if (steps < 2 || tiles(256, kBN) < kFew || tiles(256, kBN) * steps < 10 * kFew) {
+        if (most > kChain) launch_wgrad<128, kBN>(g, stream, gemm_grouped_wgrad_kernel<128, true>);
+        else launch_wgrad<128, kBN>(g, stream, gemm_grouped_wgrad_kernel<128, false>);
+    } else {
+        if (most > kChain) launch_wgrad<256, kBN>(g, stream, gemm_grouped_wgrad_kernel<256, true>);
+        else launch_wgrad<256, kBN>(g, stream, gemm_grouped_wgrad_kernel<256, false>);
+    }
 }
 
 }  // namespace ue5m3fp4
