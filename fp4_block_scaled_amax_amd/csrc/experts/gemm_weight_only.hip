@@ -119,6 +119,14 @@ __device__ __forceinline__ uint16_t to_bf16(float f) {
     return u;
 }
 
+// K up to which a wave's sum takes its terms one after another: at most 512 matrix
+// instructions (4 waves), whose roundings come to 3e-5 of sum |x w| where rows hold one or
+// two values each (random terms of one sign: 1e-6).  Beyond (LONG: 2e-4 and 1e-5 at 2^23)
+// sums of kFold are joined, and what a join rounds off begins the next one: 8e-6.  16
+// tokens, 131072 -> 4096, 130 us, 100 without.
+constexpr int64_t kChain = 65536;
+constexpr uint32_t kFold = 32;  // steps of 128 (128 matrix instructions), or chunks of a token
+
 // Where a launch's workgroups begin: row block `slot`, column tile `tile` of `tiles`.
 struct Place {
     int64_t slot;
@@ -163,7 +171,7 @@ __device__ __forceinline__ bool find_rows(const WeightOnlyArgs& a, int64_t slot,
 // the scale in its operand, another one; the scale enters once per block.  4096 ->
 // 16384 (37.7 MB) takes 8.7 us, an empty launch 2.4 us, and a kernel that only reads
 // those bytes in the same pattern 6.7 us: bound by the loads' latency and bandwidth.
-template <int ROWS, int WAVES, bool WHOLE>
+template <int ROWS, int WAVES, bool WHOLE, bool LONG>
 __global__ __launch_bounds__(64 * WAVES, 4) void one_token_kernel(WeightOnlyArgs a, Place place) {
     constexpr int kLoads = ROWS / 4;  // 4 rows of W per load
     __shared__ float sums[WAVES][ROWS];
@@ -182,9 +190,12 @@ __global__ __launch_bounds__(64 * WAVES, 4) void one_token_kernel(WeightOnlyArgs
     const uint8_t* scales = a.w_scales + (g * a.N + n0) * (a.K / 16);
     const uint16_t* x = a.x + begin * a.ldx;
 
-    float sum[kLoads];
+    float sum[kLoads], total[LONG ? kLoads : 1];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) sum[i] = 0.0f;
+    for (int i = 0; i < kLoads; ++i) {
+        sum[i] = 0.0f;
+        if constexpr (LONG) total[i] = 0.0f;
+    }
     bf16x8_t xnext[4];
     Codes next[kLoads];
     auto load = [&](uint32_t k0) __attribute__((always_inline)) {
@@ -216,7 +227,13 @@ __global__ __launch_bounds__(64 * WAVES, 4) void one_token_kernel(WeightOnlyArgs
             const float d1 = dot8(c[i].w[3], xv[3], dot8(c[i].w[2], xv[2], 0.0f));
             sum[i] = __builtin_fmaf(d0, s0 * 0x1p119f, sum[i]);
             sum[i] = __builtin_fmaf(d1, s1 * 0x1p119f, sum[i]);
+            if constexpr (LONG)
+                if (k0 / (WAVES * 512) % kFold == kFold - 1) sum[i] = fold(total[i], sum[i]);
         }
+    }
+    if constexpr (LONG) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) sum[i] = total[i] + sum[i];
     }
 
     // the 16 lanes of a row, then the waves, in a fixed order
@@ -263,7 +280,7 @@ __device__ __forceinline__ void lds_reads_done() { asm volatile("s_waitcnt lgkmc
 // 4096 -> 16384: 25.6 us, where loads straight to registers took 74 us; bound by the
 // conversions (2 instructions a weight) and by the tokens' reads, which every
 // workgroup repeats.
-template <int RT, int TOKENS, int WAVES, bool WHOLE>
+template <int RT, int TOKENS, int WAVES, bool WHOLE, bool LONG>
 __global__ __launch_bounds__(64 * WAVES, TOKENS > 32 ? 2 : 4) void tokens_kernel(WeightOnlyArgs a, Place place) {
     constexpr int kStep = 128, kUnits = 16;  // elements of K, and units of a token, per step
     constexpr int TT = (TOKENS + 15) / 16;
@@ -291,11 +308,14 @@ __global__ __launch_bounds__(64 * WAVES, TOKENS > 32 ? 2 : 4) void tokens_kernel
 #pragma unroll
     for (int i = 0; i < RT; ++i) row[i] = (uint32_t)min(16 * i + r, rows - 1);
 
-    f32x4_t acc[RT][TT];
+    f32x4_t acc[RT][TT], total[LONG ? RT : 1][LONG ? TT : 1];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int t = 0; t < TT; ++t) acc[i][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int t = 0; t < TT; ++t) {
+            acc[i][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (LONG) total[i][t] = acc[i][t];
+        }
 
     // load i brings tokens 4 i .. 4 i + 3; places of tokens that are not there
     // repeat the last one, units past K the last one of the row
@@ -358,6 +378,19 @@ __global__ __launch_bounds__(64 * WAVES, TOKENS > 32 ? 2 : 4) void tokens_kernel
             // the next codes into the registers that are free now
             if (more) load_codes(w[i], codes, scales, row[i], K, k0 + kStep + 32 * q, WHOLE || k0 + 2 * kStep <= K);
         }
+        if constexpr (LONG)
+            if (j % kFold == kFold - 1 || !more)
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int t = 0; t < TT; ++t)
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            float s = total[i][t][d];
+                            const float lost = fold(s, acc[i][t][d]);
+                            total[i][t][d] = s;
+                            acc[i][t][d] = more ? lost : s;
+                        }
     }
 
     // ---- join the waves' sums: lane (r, q) holds rows 4 q .. 4 q + 3 of W for token r
@@ -574,13 +607,13 @@ __global__ __launch_bounds__(64 * WAVES, RT > 2 ? 2 : RT * TOKENS >= 32 ? 3 : 4)
     }
 }
 
-template <int ROWS, int WAVES>
+template <int ROWS, int WAVES, bool LONG = false>
 void launch_one(const WeightOnlyArgs& a, hipStream_t stream) {
     const int64_t tiles_n = (a.N + ROWS - 1) / ROWS;
     in_launches(a.rows * tiles_n, 64 * WAVES, [&](int64_t first, dim3 grid) {
         const Place at{first / tiles_n, (uint32_t)(first % tiles_n), (uint32_t)tiles_n};
-        if (a.K % 512 == 0) hipLaunchKernelGGL((one_token_kernel<ROWS, WAVES, true>), grid, dim3(64 * WAVES), 0, stream, a, at);
-        else hipLaunchKernelGGL((one_token_kernel<ROWS, WAVES, false>), grid, dim3(64 * WAVES), 0, stream, a, at);
+        if (!LONG && a.K % 512 == 0) hipLaunchKernelGGL((one_token_kernel<ROWS, WAVES, true, false>), grid, dim3(64 * WAVES), 0, stream, a, at);
+        else hipLaunchKernelGGL((one_token_kernel<ROWS, WAVES, false, LONG>), grid, dim3(64 * WAVES), 0, stream, a, at);
     });
 }
 
@@ -596,15 +629,15 @@ void launch_chunks(const WeightOnlyArgs& a, hipStream_t stream) {
     });
 }
 
-template <int RT, int TOKENS, int WAVES>
+template <int RT, int TOKENS, int WAVES, bool LONG = false>
 void launch(const WeightOnlyArgs& a, hipStream_t stream) {
     const int64_t tiles_n = (a.N + 16 * RT - 1) / (16 * RT);
     int64_t slots = (a.rows + TOKENS - 1) / TOKENS;
     if (a.offsets) slots = a.rows / TOKENS + (a.experts < a.rows ? a.experts : a.rows);
     in_launches(slots * tiles_n, 64 * WAVES, [&](int64_t first, dim3 grid) {
         const Place at{first / tiles_n, (uint32_t)(first % tiles_n), (uint32_t)tiles_n};
-        if (a.K % 128 == 0) hipLaunchKernelGGL((tokens_kernel<RT, TOKENS, WAVES, true>), grid, dim3(64 * WAVES), 0, stream, a, at);
-        else hipLaunchKernelGGL((tokens_kernel<RT, TOKENS, WAVES, false>), grid, dim3(64 * WAVES), 0, stream, a, at);
+        if (!LONG && a.K % 128 == 0) hipLaunchKernelGGL((tokens_kernel<RT, TOKENS, WAVES, true, false>), grid, dim3(64 * WAVES), 0, stream, a, at);
+        else hipLaunchKernelGGL((tokens_kernel<RT, TOKENS, WAVES, false, LONG>), grid, dim3(64 * WAVES), 0, stream, a, at);
     });
 }
 
@@ -629,7 +662,11 @@ void launch_gemm_weight_only(const WeightOnlyArgs& a, hipStream_t stream) {
     // Workgroups that 16 rows of W each would make.
     const int64_t blocks = a.offsets ? (a.experts < a.rows ? a.experts : a.rows) : (a.rows + 63) / 64;
     const int64_t groups = (a.N + 15) / 16 * blocks;
-    if (each == 1) {
+    if (a.K > kChain) {
+        if (each == 1) launch_one<16, 8, true>(a, stream);
+        else if (each <= 16) launch<1, 16, 8, true>(a, stream);
+        else launch<1, 64, 8, true>(a, stream);
+    } else if (each == 1) {
         if (groups >= 2048 && a.K <= 1024) launch_one<16, 2>(a, stream);
         else if (groups >= 1024 && a.K <= 5120) launch_one<16, 4>(a, stream);
         else launch_one<16, 8>(a, stream);

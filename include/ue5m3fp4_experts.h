@@ -39,6 +39,12 @@
  * experts of a larger operand: codes have to be 8-byte aligned, scales 8-byte
  * where C is a multiple of 128, else not at all.
  *
+ * Sums.  Products are exact and sums are fp32.  A sum passes at most 2048
+ * roundings one after another: longer contractions are joined from shorter
+ * sums whose roundings are carried on.  So a result is off by at most 2^-13 of
+ * |ts| sum|a b| however long the contraction and whatever the terms, and by
+ * less than 1e-5 of it where they are not alike (rounding to bf16 comes on top).
+ *
  * Conventions: those of include/ue5m3fp4.h -- device pointers owned by the
  * caller, every argument checked on the host before any HIP call, work
  * enqueued on `stream` of the current device, nothing allocated, synchronized
