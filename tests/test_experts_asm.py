@@ -1,9 +1,13 @@
-"""CPU test of the waits in the experts' kernels whose loads go straight to LDS:
-the compiler knows neither when such a load ends nor what it overwrites, so a
-wave waits for its LDS reads before it asks for anything in their place."""
+"""CPU tests of the experts' kernels whose loads go straight to LDS: the compiler
+knows neither when such a load ends nor what it overwrites, so a wave waits for
+its LDS reads before it asks for anything in their place, and the statements say
+what they write."""
 
+import glob
 import os
 import re
+
+import test_layer_asm
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "fp4_block_scaled_amax_amd", "csrc", "experts")
@@ -51,3 +55,18 @@ def test_reads_end_before_their_place_is_loaded_again():
         assert any(governs(loop, w, at) for w in waits), k.group(1)
         seen.append(k.group(1))
     assert sorted(seen) == ["chunks_kernel", "tokens_kernel"]
+
+
+def test_loads_to_lds_say_what_they_write(monkeypatch):
+    """Every statement that writes m0 has it as an output, what touches memory or waits is volatile and clobbers memory,
+    and a load to LDS stands five wait states behind the vector instruction that may have written its scalar base."""
+    monkeypatch.setattr(test_layer_asm, "SOURCES", sorted(glob.glob(os.path.join(CSRC, "*.h*"))))
+    loads = 0
+    for name, volatile, text, outputs, clobbers in test_layer_asm.statements():
+        assert ("m0" in text) == ('"=&{m0}"' in outputs) and '"m0"' not in clobbers, (name, text)
+        if "s_waitcnt" in text or re.search(r"\b(global|buffer|flat|ds)_(load|store|read|write|atomic)\w*", text):
+            assert volatile and '"memory"' in clobbers, (name, text)
+        if "_lds_" in text:
+            assert re.match(r'\s*"s_mov_b32 m0, %\d\s+s_nop 4\s+global_load_lds_', text), (name, text)
+            loads += 1
+    assert loads == 3
