@@ -89,6 +89,10 @@ __device__ __forceinline__ int64_t padded_begin(int begin, int g) {
     return 128 * (((int64_t)begin + 127) / 128 + g);
 }
 
+// The scale of a sum of K terms.  Of none it is 0 under any tensor scale, NaN and the
+// infinities (which 0 times them would not be) among them.
+__device__ __forceinline__ float scale_of_sum(float ts, int64_t K) { return K > 0 ? ts : __builtin_copysignf(1.0f, ts); }
+
 // sum + part; returns what that rounds off, which belongs to the next part (nothing of an
 // infinity or NaN).
 __device__ __forceinline__ float fold(float& sum, float part) {

@@ -711,8 +711,8 @@ __device__ __forceinline__ bool nt_tile(const GemmGroupedArgs& g, Tile& t) {
     t.rows = (int)min(end - m0, (int64_t)BM);
     t.cols = (int)min(g.N - n0, (int64_t)BN);
     t.c = m0 * g.N + n0;
-    t.sa256 = *g.a_ts * 256.0f;
-    t.sb = g.b_ts[expert * g.b_ts_step];
+    t.sa256 = scale_of_sum(*g.a_ts * 256.0f, t.K);
+    t.sb = scale_of_sum(g.b_ts[expert * g.b_ts_step], t.K);
     return true;
 }
 
@@ -745,8 +745,8 @@ __device__ __forceinline__ void wgrad_tile(const GemmGroupedArgs& g, Tile& t) {
     t.rows = (int)min(g.M - m0, (int64_t)BM);
     t.cols = (int)min(g.N - n0, (int64_t)BN);
     t.c = (expert * g.M + m0) * g.N + n0;
-    t.sa256 = *g.a_ts * 256.0f;
-    t.sb = *g.b_ts;
+    t.sa256 = scale_of_sum(*g.a_ts * 256.0f, t.K);
+    t.sb = scale_of_sum(*g.b_ts, t.K);
 }
 
 template <int BM, bool WHOLE, bool LONG>

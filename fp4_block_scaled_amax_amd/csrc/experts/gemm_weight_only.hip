@@ -181,7 +181,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void one_token_kernel(WeightOnlyArgs
     if (!find_rows(a, slot, 1, g, begin, end)) return;
     g = __builtin_amdgcn_readfirstlane(g);
     begin = __builtin_amdgcn_readfirstlane(begin);
-    const float ts = a.w_ts[g * a.w_ts_step];
+    const float ts = scale_of_sum(a.w_ts[g * a.w_ts_step], a.K);
     const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t K = (uint32_t)a.K;
@@ -294,7 +294,7 @@ __global__ __launch_bounds__(64 * WAVES, TOKENS > 32 ? 2 : 4) void tokens_kernel
     begin = __builtin_amdgcn_readfirstlane(begin);
     end = __builtin_amdgcn_readfirstlane(end);
     const int tokens = min(end - begin, TOKENS);
-    const float ts = a.w_ts[g * a.w_ts_step];
+    const float ts = scale_of_sum(a.w_ts[g * a.w_ts_step], a.K);
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
@@ -481,7 +481,7 @@ __global__ __launch_bounds__(64 * WAVES, RT > 2 ? 2 : RT * TOKENS >= 32 ? 3 : 4)
     begin = __builtin_amdgcn_readfirstlane(begin);
     end = __builtin_amdgcn_readfirstlane(end);
     const int tokens = min(end - begin, TOKENS);
-    const float ts = a.w_ts[g * a.w_ts_step];
+    const float ts = scale_of_sum(a.w_ts[g * a.w_ts_step], a.K);
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t K = (uint32_t)a.K;
