@@ -261,15 +261,20 @@ def gemm_grouped_dgrad(dy_row, w_col, offsets, dx, amax=None, stream=None):
     return _gemm_grouped(dy_row, w_col, offsets, dx, amax, stream, "dy_row", "w_col")
 
 
-def gemm_grouped_wgrad(dy_col, x_col, offsets, dw, stream=None):
+def gemm_grouped_wgrad(dy_col, x_col, offsets, dw, stream=None, rows=None):
     """dW [experts][out][in] (bf16 or fp32) = dY^T X over each expert's rows,
     from the grouped transposed operands of dY and X; zeros for an expert
-    without rows."""
+    without rows.  rows: how many the operands were quantized from, to which
+    offsets past them are clamped as they were there.  Their columns tell it up
+    to a multiple of 128 alone, so it is needed where offsets may pass the rows;
+    where they do not, it changes nothing."""
     device = _device(dw, "dw")
     experts = _experts(offsets, device)
     (M, padded), (N, x_padded) = _operand(dy_col, device, "dy_col"), _operand(x_col, device, "x_col")
-    rows = padded - 128 * experts  # up to a multiple of 128, which rows_padded does not tell apart
-    if rows < 0 or rows % 128 != 0 or x_padded != padded:
+    whole = padded - 128 * experts
+    if rows is None:
+        rows = whole
+    if rows < 0 or whole % 128 != 0 or whole != 128 * ((rows + 127) // 128) or x_padded != padded:
         raise ValueError(f"dy_col and x_col must have rows_padded(rows, {experts}) columns "
                          f"(have {padded} and {x_padded})")
     f32 = _result(dw, device, (experts, M, N), "dw")

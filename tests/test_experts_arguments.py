@@ -1,0 +1,27 @@
+"""CPU tests of arguments that the experts' binding takes as well as refuses."""
+
+import pytest
+
+import fp4_block_scaled_amax_amd as lib
+from test_binding_checks import Dev, raises
+from test_experts_checks import dev, offs, quantized
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    seen = []
+    monkeypatch.setattr(Dev, "data_ptr", lambda self: 64)
+    monkeypatch.setattr(lib.experts, "_launch", lambda where, device, stream, *args: seen.append((where, args)))
+    return seen
+
+
+def test_wgrad_takes_its_number_of_rows(calls):
+    o, dw, a, b = offs(2), dev(2, 48, 64), quantized(48, 384), quantized(64, 384)
+    for rows, taken in ((None, 128), (128, 128), (70, 70), (1, 1)):
+        lib.gemm_grouped_wgrad(a, b, o, dw, rows=rows)
+        where, args = calls.pop()
+        assert where == "ue5m3fp4_gemm_grouped_wgrad" and args[7:9] == (2, taken)
+    for rows in (0, 129, -1):
+        raises(lambda: lib.gemm_grouped_wgrad(a, b, o, dw, rows=rows), "rows_padded")
+    lib.gemm_grouped_wgrad(quantized(48, 256), quantized(64, 256), o, dw, rows=0)
+    assert calls.pop()[1][7:9] == (2, 0)

@@ -43,3 +43,30 @@ def test_products_of_no_elements_are_zero_under_any_scale(cuda_device, rows, N, 
                 y = empty((n, N), bf16)
                 lib.gemm_weight_only(torch.empty((n, 0), dtype=torch.bfloat16, device="cuda"), w.expert(1), y)
                 assert bool((y == 0).all())
+
+
+def test_wgrad_clamps_offsets_to_the_rows_it_is_given(cuda_device):
+    """Offsets past the rows of the operands: quantizer and wgrad have to clamp them to the same number of rows, or wgrad
+    reads columns that the quantizer never wrote."""
+    import torch
+
+    width, ts = 48, dev_scalar(0.01)
+    for rows, raw, held in ((70, [0, 40, 70, 2 ** 31 - 1], [0, 40, 70, 70]), (130, [0, 100, 100, 1000], [0, 100, 100, 130]),
+                            (129, [-5, 128, 500, 600], [0, 128, 129, 129]), (128, [0, 1, 90, 300], [0, 1, 90, 128])):
+        P = lib.rows_padded(rows, 3)
+        x = torch.randn((rows, width), device="cuda", generator=torch.Generator("cuda").manual_seed(1)).bfloat16()
+
+        def operand():
+            u8 = dict(dtype=torch.uint8, device="cuda")
+            return lib.Quantized(torch.full((width, P // 2), 0x77, **u8), torch.full((width, P // 16), 0xFF, **u8), ts)
+
+        got, want = empty((3, width, width), False), empty((3, width, width), False)
+        for o, dw in ((dev_i32(raw), got), (dev_i32(held), want)):
+            q = operand()
+            lib.quantize_grouped(x, o, ts, col=q)
+            lib.gemm_grouped_wgrad(q, q, o, dw, rows=rows)
+        assert bool(want.isfinite().all()) and torch.equal(got, want)
+        q = operand()
+        lib.quantize_grouped(x, dev_i32(held), ts, col=q)
+        lib.gemm_grouped_wgrad(q, q, dev_i32(held), got)  # offsets inside the rows need no count of them
+        assert torch.equal(got, want)
