@@ -79,6 +79,7 @@ class ExpertWeights:
     def expert(self, g):
         """Expert g's operand (views), for gemm_weight_only, and as an output of quantize_blockscale or an operand of
         the other products where R * C / 16 is a multiple of 16 (they need 16-byte aligned scales)."""
+        g = range(self.experts)[g]
         return Quantized(self.codes[g], self.scales[g], self.ts[g:g + 1] if self.ts.numel() > 1 else self.ts)
 
 

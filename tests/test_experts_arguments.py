@@ -1,6 +1,7 @@
 """CPU tests of arguments that the experts' binding takes as well as refuses."""
 
 import pytest
+import torch
 
 import fp4_block_scaled_amax_amd as lib
 from test_binding_checks import Dev, raises
@@ -25,3 +26,14 @@ def test_wgrad_takes_its_number_of_rows(calls):
         raises(lambda: lib.gemm_grouped_wgrad(a, b, o, dw, rows=rows), "rows_padded")
     lib.gemm_grouped_wgrad(quantized(48, 256), quantized(64, 256), o, dw, rows=0)
     assert calls.pop()[1][7:9] == (2, 0)
+
+
+def test_an_expert_counted_from_the_end():
+    w = lib.empty_expert_weights(3, 10, 32, torch.ones(3))
+    for g in (-1, -2, -3):
+        q, want = w.expert(g), w.expert(3 + g)
+        assert q.ts.numel() == 1 and q.ts.data_ptr() == want.ts.data_ptr()
+        assert q.codes.data_ptr() == want.codes.data_ptr() and q.scales.data_ptr() == want.scales.data_ptr()
+    for g in (3, -4):
+        with pytest.raises(IndexError):
+            w.expert(g)
