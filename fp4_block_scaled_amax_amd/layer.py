@@ -74,7 +74,7 @@ def _enqueue(fn, where, device, stream, *args):
         raise ValueError(f"{where}: the stream belongs to {stream.device}, the tensors are on {device}")
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch._C._cuda_getDevice() == device.index:
+    if torch.cuda.current_device() == device.index:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(device):

@@ -37,3 +37,26 @@ def test_an_expert_counted_from_the_end():
     for g in (3, -4):
         with pytest.raises(IndexError):
             w.expert(g)
+
+
+def test_calls_run_with_their_device_current(monkeypatch):
+    """The libraries launch on the current device: it is asked for, and changed for the call where it is another."""
+    log = []
+
+    class Current:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            log.append(("enter", self.d.index))
+
+        def __exit__(self, *exc):
+            log.append("exit")
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "device", Current)
+    launch = lambda *args: log.append(args) or 0  # noqa: E731
+    lib.layer._enqueue(launch, "f", torch.device("cuda:1"), 5, 7)
+    assert log == [(7, 5)]
+    lib.layer._enqueue(launch, "f", torch.device("cuda:0"), 5, 7)
+    assert log[1:] == [("enter", 0), (7, 5), "exit"]
