@@ -165,7 +165,7 @@ __device__ __forceinline__ bool find_rows(const WeightOnlyArgs& a, int64_t slot,
 
 // One token per workgroup.  16 lanes share a row of W: each has 32 consecutive
 // codes of a chunk of 512 (a row's 256 bytes are read together) and the same 32
-// elements of the token, which it keeps in registers for all rows.  The 8 waves
+// elements of the token, which it keeps in registers for all rows.  The waves
 // share out the chunks.  Products in v_dot2_f32_bf16, which with the conversion to
 // bf16 costs one instruction per weight, where the matrix instruction would need
 // the scale in its operand, another one; the scale enters once per block.  4096 ->
@@ -276,10 +276,13 @@ __device__ __forceinline__ void lds_reads_done() { asm volatile("s_waitcnt lgkmc
 // 16, lane / 16) has 32 consecutive codes of row r and the same 32 elements of token
 // r.  A wave brings its own step's tokens to LDS, in whole lines, while it multiplies
 // the step before; unit u (16 bytes) of token t stands at u ^ (t % 16) of the
-// token's 256 bytes, so that 16 tokens read a unit without bank conflicts.  64 tokens,
-// 4096 -> 16384: 25.6 us, where loads straight to registers took 74 us; bound by the
-// conversions (2 instructions a weight) and by the tokens' reads, which every
-// workgroup repeats.
+// token's 256 bytes, since without it 16 tokens would meet in the same banks.  Two
+// still do (a 16-byte read serves lanes 0-3, 12-15 and 20-27 together); places
+// without any conflict changed no time.  64 tokens, 4096 -> 16384: 26 us, where loads straight
+// to registers took 74 us; bound by the conversions (2 instructions a weight), by the
+// tokens' reads, which every workgroup repeats, and by the weights: a row block's next
+// codes go into the registers of the ones just multiplied, so the last block's are asked for
+// right before the wait for the tokens, and arrive while nothing is multiplied.
 template <int RT, int TOKENS, int WAVES, bool WHOLE, bool LONG>
 __global__ __launch_bounds__(64 * WAVES, TOKENS > 32 ? 2 : 4) void tokens_kernel(WeightOnlyArgs a, Place place) {
     constexpr int kStep = 128, kUnits = 16;  // elements of K, and units of a token, per step
@@ -465,7 +468,10 @@ __device__ __forceinline__ u32x2 dealt(u32x2 s, uint32_t pick) {
 // The same in chunks of 4 steps: fewer loads of scales, and all of a chunk's codes
 // are on their way at once.  The tokens of PART steps stand in LDS; they are read
 // into registers before the next ones are asked for, or (4 tokens) have two places.
-// 16 tokens, 16384 -> 4096: 16.4 us (2.3 TB/s), in steps of 128 it took 32 us.
+// 16 tokens, 16384 -> 4096: 16.7 us (2.3 TB/s), in steps of 128 it took 32 us; the bytes
+// alone would take 7.5.  With RT = 1 a wave asks for its next chunk behind its last
+// product and then waits for all loads, so it has no weights in flight while it
+// multiplies, and a CU has two such waves per SIMD.
 template <int RT, int TOKENS, int WAVES, bool WHOLE>
 __global__ __launch_bounds__(64 * WAVES, RT > 2 ? 2 : RT * TOKENS >= 32 ? 3 : 4) void chunks_kernel(WeightOnlyArgs a, Place place) {
     constexpr int kChunk = 512, PART = TOKENS > 4 ? 2 : 4, kPlaces = TOKENS > 4 ? 1 : 2;
@@ -511,7 +517,7 @@ __global__ __launch_bounds__(64 * WAVES, RT > 2 ? 2 : RT * TOKENS >= 32 ? 3 : 4)
                 load_to_lds(x, 2 * (min(t, (uint32_t)tokens - 1) * (uint32_t)a.ldx + k), at + s * kStepBytes + 1024 * i);
             }
     };
-    // chunk j of this wave is chunk wave + 8 j of K
+    // chunk j of this wave is chunk wave + WAVES j of K
     const uint32_t first = wave * kChunk, stride = WAVES * kChunk;
     ChunkCodes w[RT];
     if (first < K) {
@@ -646,15 +652,41 @@ void launch(const WeightOnlyArgs& a, hipStream_t stream) {
 // What a workgroup has.  Rows of W: joining 32 or 64 halves the reads of the tokens, and
 // workgroups.  Waves, which share out K: 8 have the most loads in flight where there are
 // few workgroups (16384 -> 4096, 4 tokens, 12.7 us, with 4 waves 16.5); where there are
-// many, fewer leave none idle when K is short and join fewer sums.  Measured, us:
-//   1 token    4096 -> 16384        16 rows, 8 waves  9.9   16 rows, 4 waves  8.7
-//              16 of 64 experts 1024 -> 4096  16, 8  21.1       16, 2        10.8 (16, 4: 13.1)
-//   16 tokens  1024 -> 16384            16, 8         8.6       32, 4         6.8
-//              9 experts 2064 -> 1305   32, 8        12.8       16, 4         9.0
-//              64 experts 4096 -> 2048  64, 8        92.6       32, 4        68.0
-//              64 experts 1024 -> 4096  16, 8       131         64, 2        43.9 (32, 4: 50.4)
-//   64 tokens  4096 -> 16384            16, 8        37.8       32, 4        25.7
-//              64 experts 1024 -> 4096  16, 8       280         32, 2        96.4 (32, 4: 110)
+// many, fewer leave none idle when K is short and join fewer sums.  Experts, us:
+//   1 token    16 of 64 experts 1024 -> 4096  16 rows, 8 waves 21.1   16, 2  10.8   16, 4  13.1
+//   16 tokens  9 experts 2064 -> 1305         32, 8  12.8             16, 4   9.0
+//              64 experts 4096 -> 2048        64, 8  92.6             32, 4  68.0
+//              64 experts 1024 -> 4096        16, 8 131               64, 2  43.9   32, 4  50.4
+//   64 tokens  64 experts 1024 -> 4096        16, 8 280               32, 2  96.4   32, 4 110
+// One matrix, on both sides of the borders below, us (workgroups that 16 rows each make):
+//                        256    384    512    768   1024   1536   2048   4096
+//   1 token   16, 8                    6.1    8.6    9.8   13.6   17.2   31.5   K = 4096
+//             16, 4                    6.0    7.6    8.7   11.7   14.9   26.8
+//             16, 8                    9.7   14.5   16.4   23.1   29.4   54.5   K = 8192
+//             16, 4                   10.4   13.9   17.1   24.5   30.8   56.9
+//             16, 4                    3.9    4.1    4.5    6.1    7.0   10.9   K = 1024
+//             16, 2                    3.9    4.2    4.3    5.6    6.1    9.0
+//             16, 4                    4.2    4.7    5.4    7.0    8.2   12.8   K = 1536
+//             16, 2                    4.4    4.8    5.6    6.9    7.9   13.1
+//   4 tokens  16, 8      5.5    7.7    8.0   10.6   13.2   18.8   23.8   45.2   K = 4096
+//             16, 4      6.1    7.8    8.0   10.5   12.0   16.9   20.6   36.4
+//             32, 4      8.2    8.9    9.3   11.6   12.0   16.4   19.5   33.7
+//             32, 4                                  6.8    7.7    8.6   14.3   K = 1024
+//             32, 2                                  6.7    7.9    8.3   11.5
+//   16 tokens 16, 8      6.2    9.8   10.1   14.0   17.1   23.9   30.3   56.7   K = 4096
+//             16, 4      6.5    9.4    9.7   13.3   16.2   22.9   28.6   53.1
+//             32, 4      8.3    9.4   10.0   13.8   14.4   19.0   23.7   44.4
+//             32, 4                                  6.7    8.0    9.1   15.4   K = 1024
+//             64, 2                                  7.5   10.6   10.9   14.3
+//   32 tokens 16, 8      7.2   13.9   14.3   19.9   25.2   36.6   47.3   90.3   K = 4096
+//             32, 4     10.2   12.2   12.8   19.5   20.1   28.7   37.1   70.4
+//   64 tokens 16, 8     10.0   20.0   20.9   29.7   38.3   56.4   74.0  145     K = 4096
+//             32, 4     12.8   14.8   15.7   26.1   26.4   38.2   48.6   91.5
+//             32, 4                    6.7    9.0    9.1   14.6   17.1   31.0   K = 1024
+//             32, 2                    8.4    9.8   10.0   13.4   16.1   31.6
+// The forms cross where the rule changes or are within a tenth of each other there, but
+// for 8 waves kept from 512 to 1024 (1 token) and from 256 to 512 (32 and 64
+// tokens), which cost up to a third there, and 64 rows at 2048 of K = 1024, a fifth.
 void launch_gemm_weight_only(const WeightOnlyArgs& a, hipStream_t stream) {
     // Tokens that a workgroup should be ready for: all, or of an expert twice the
     // mean (more than that take the weights a second time).

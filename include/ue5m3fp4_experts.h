@@ -78,7 +78,8 @@ enum ue5m3fp4_output_type { UE5M3FP4_OUT_BF16 = 0, UE5M3FP4_OUT_F32 = 1 };
  *       stream counts elements of the rows x cols matrix, the transposed one
  *       those of the cols x rows_padded matrix);
  *   amax_inout: nullable; receives max(*amax_inout, max|x|) over the experts'
- *       rows (a NaN propagates).
+ *       rows (a NaN propagates).  It starts at 0 or an earlier amax: values with
+ *       a sign, -0 included, are kept as they are (so in the products, too).
  * Each pair is both NULL or both non-NULL, at least one of the pairs and
  * amax_inout non-NULL; tensor_scale may be NULL without pairs.
  * cols % 16 == 0 (ESHAPE), ld >= cols (ESHAPE), ld % 8 == 0 (EALIGN); rows,
@@ -110,6 +111,8 @@ UE5M3FP4_API int ue5m3fp4_gemm_grouped_nt(const uint8_t* a_codes, const uint8_t*
  * its rows have in the grouped transposed operands,
  *   C_g[i][j] = (tsA * tsB) * sum_p A(i, p) * B(j, p),  fp32 accumulation.
  *   a: M x rows_padded (dY's transposed output); b: N x rows_padded (X's);
+ *   rows: those that the operands were quantized from (offsets are clamped to
+ *       them in both places, so the numbers have to agree);
  *   c: [experts][M][N], bf16 or fp32; an expert without rows gets zeros.
  * M, N < 2^31, rows_padded < 2^24; M * rows_padded, N * rows_padded and experts
  * * M * N < 2^40 (ERANGE). */
